@@ -26,6 +26,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "hkv_host.h"
 #include "hkv_kernels.cuh"
 
 namespace hkv {
@@ -590,11 +591,11 @@ struct WsLayout {
 
 static size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-static int es_of(hkv_dtype d) { return d == HKV_BF16 ? 2 : 4; }
+int es_of(hkv_dtype d) { return d == HKV_BF16 ? 2 : 4; }
 
 // The driver's tensor-map encoder, looked up once through the runtime
 // (nullptr when the driver does not provide it).
-static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         void *p = nullptr;
@@ -643,7 +644,7 @@ static void set_row_maps(const hkv_problem *p, const hkv_tier *sparse, Params &P
     P.vmap_ok = ok ? 1 : 0;
 }
 
-static hkv_status check_tier(const hkv_tier *t, const hkv_problem *p, bool need_v)
+hkv_status check_tier(const hkv_tier *t, const hkv_problem *p, bool need_v)
 {
     if (t == nullptr)
         return HKV_OK;
@@ -663,7 +664,7 @@ static hkv_status check_tier(const hkv_tier *t, const hkv_problem *p, bool need_
     return HKV_OK;
 }
 
-static hkv_status check_problem(const hkv_problem *p)
+hkv_status check_problem(const hkv_problem *p)
 {
     if (p == nullptr)
         return HKV_ERR_INVALID_ARG;
@@ -687,7 +688,7 @@ static hkv_status check_problem(const hkv_problem *p)
     return HKV_OK;
 }
 
-static int sm_count()
+int sm_count()
 {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -800,7 +801,7 @@ static std::mutex g_mu;
 static KernelInfo g_info[256];
 static int g_ninfo = 0;
 
-static hkv_status prepare(const void *fn, int threads, size_t smem, int *blocks_per_sm)
+hkv_status prepare(const void *fn, int threads, size_t smem, int *blocks_per_sm)
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess)

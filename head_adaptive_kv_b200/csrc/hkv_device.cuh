@@ -121,7 +121,7 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
 // Slow path of mbar_wait: spin at most wait_ns nanoseconds. On expiry the
 // status word gets HKV_DEV_TIMEOUT and every later wait in any CTA returns
 // false at once.
-__device__ __noinline__ bool mbar_wait_slow(uint64_t *bar, uint32_t parity, uint32_t *status, uint64_t wait_ns)
+static __device__ __noinline__ bool mbar_wait_slow(uint64_t *bar, uint32_t parity, uint32_t *status, uint64_t wait_ns)
 {
     const uint64_t t0 = global_ns();
     for (uint32_t it = 1;; ++it) {
@@ -141,7 +141,7 @@ __device__ __noinline__ bool mbar_wait_slow(uint64_t *bar, uint32_t parity, uint
 // Wait at most wait_ns for the phase of `bar` with the given parity, whatever
 // the status word says (used to let copies already started land before a CTA
 // exits after a timeout).
-__device__ __noinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity, uint64_t wait_ns)
+static __device__ __noinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity, uint64_t wait_ns)
 {
     const uint64_t t0 = global_ns();
     for (uint32_t it = 1;; ++it) {
