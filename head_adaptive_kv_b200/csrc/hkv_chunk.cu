@@ -1,0 +1,342 @@
+// hkv_chunk.cu -- attention of a chunk of new tokens over the paged cache
+// (C ABI in hkv_prompt.h). The work line and the merge are in hkv_chunk.cuh.
+#include <algorithm>
+#include <cmath>
+
+#include <cuda_bf16.h>
+
+#include "hkv_chunk.cuh"
+#include "hkv_host.h"
+
+namespace hkv {
+
+// =============================================================================
+// 32-bit kernel: fp32 products on the FMA units
+//
+// 16 x 16 threads; thread (y, x) holds rows y + 16 i and, of a tile's 64 keys,
+// x + 16 j; of the output columns 4 x + 64 c. K and V tiles land by cp.async;
+// the weights take K's place in shared memory once the scores are formed.
+// M = 64 rows an item for prompts, 16 where single tokens make up the batch.
+// =============================================================================
+
+constexpr int FC_NT = 256;
+constexpr int FC_NK = 64;
+
+template <int ES>
+__device__ __forceinline__ float4 widen4(const char *p);
+template <>
+__device__ __forceinline__ float4 widen4<4>(const char *p)
+{
+    return *reinterpret_cast<const float4 *>(p);
+}
+template <>
+__device__ __forceinline__ float4 widen4<2>(const char *p)
+{
+    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+    const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+
+template <int D, int M>
+struct FcSmem {
+    float q[M][D + 4];
+    float k[FC_NK][D + 4];  // then the weights, [M][FC_NK + 4]
+    float v[FC_NK][D];
+    ChunkShare share;
+    unsigned long long red[FC_NT / 32];
+    int ok[FC_NK];  // the tile's keys that are there
+};
+
+template <int ES, int D, int M>
+__global__ void __launch_bounds__(FC_NT, 2) k_chunk_fma(const __grid_constant__ ChunkP P)
+{
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    auto &sm = *reinterpret_cast<FcSmem<D, M> *>(smem_raw);
+    constexpr int RT = M / 16, CT = D / 64;
+    static_assert(M * (FC_NK + 4) <= FC_NK * (D + 4), "the weights fit in K's place");
+    float(*w)[FC_NK + 4] = reinterpret_cast<float(*)[FC_NK + 4]>(&sm.k[0][0]);
+    wait_prior_grid();
+    const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+    if (tid == 0)
+        P.desc[blockIdx.x].n = 0;
+    chunk_share<FC_NT, M, FC_NK>(P, sm.red, &sm.share);
+    const int G = 1 << P.g_log2;
+    const int64_t rec = (int64_t)P.rec_rows * (D + 2);
+    bool bad = false;
+    for (ChunkWalk<M, FC_NK> it(P, sm.share); it.item(); it.next()) {
+        if (!it.mine())
+            continue;
+        __syncthreads();  // the item before is done with q
+        for (int i = tid; i < M * (D / 4); i += FC_NT) {
+            const int r = i / (D / 4), x = i % (D / 4);
+            float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < it.rows)
+                val = widen4<ES>(P.q + (it.row0 + (r >> P.g_log2)) * P.qs +
+                                 ((int64_t)(it.h * G + (r & (G - 1))) * D + 4 * x) * ES);
+            *reinterpret_cast<float4 *>(&sm.q[r][4 * x]) = val;
+        }
+        float mx[RT], sum[RT];
+        float4 o[RT][CT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            mx[i] = -INFINITY;
+            sum[i] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+                o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        for (int j = it.j0; j < it.j1; ++j) {
+            const int key0 = j * FC_NK;
+            __syncthreads();  // the tile before is done with k, v and ok
+            for (int i = tid; i < FC_NK * (D / 4); i += FC_NT) {
+                const int r = i / (D / 4), x = i % (D / 4), key = key0 + r;
+                const int p = key < it.r.kv ? page_of(P.pages, it.b, key) : -1;
+                if (x == 0) {
+                    sm.ok[r] = p >= 0;
+                    bad = bad || (p < 0 && key < it.r.kv);
+                }
+                float4 kk = make_float4(0.f, 0.f, 0.f, 0.f), vv = kk;
+                if (p >= 0) {
+                    const int64_t at = row_offset(P.pages, p, it.h, key) + 4 * x * ES;
+                    kk = widen4<ES>(P.pages.k + at);
+                    vv = widen4<ES>(P.pages.v + at);
+                }
+                *reinterpret_cast<float4 *>(&sm.k[r][4 * x]) = kk;
+                *reinterpret_cast<float4 *>(&sm.v[r][4 * x]) = vv;
+            }
+            __syncthreads();
+            float s[RT][4];
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    s[i][n] = 0.0f;
+#pragma unroll 4
+            for (int d = 0; d < D; d += 4) {
+                float4 a[RT], b[4];
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+                    a[i] = lds4(&sm.q[ty + 16 * i][d]);
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    b[n] = lds4(&sm.k[tx + 16 * n][d]);
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        s[i][n] = fmaf(a[i].x, b[n].x,
+                                       fmaf(a[i].y, b[n].y, fmaf(a[i].z, b[n].z, fmaf(a[i].w, b[n].w, s[i][n]))));
+            }
+            int ok[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                ok[n] = sm.ok[tx + 16 * n];
+            __syncthreads();  // k has been read: the weights take its place
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                const int pos = it.pos0 + ((ty + 16 * i) >> P.g_log2);
+                float top = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const bool on = ok[n] && key0 + tx + 16 * n <= pos;
+                    s[i][n] = on ? s[i][n] * P.scale_log2 : -INFINITY;
+                    top = fmaxf(top, s[i][n]);
+                }
+#pragma unroll
+                for (int x = 8; x > 0; x >>= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                const float mn = fmaxf(mx[i], top);
+                const float ref = mn == -INFINITY ? 0.0f : mn;  // nothing yet: all weights 0
+                const float f = ex2(mx[i] - ref);
+                mx[i] = mn;
+                sum[i] *= f;
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+                    o[i][c].x *= f;
+                    o[i][c].y *= f;
+                    o[i][c].z *= f;
+                    o[i][c].w *= f;
+                }
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const float p = ex2(s[i][n] - ref);
+                    sum[i] += p;
+                    w[ty + 16 * i][tx + 16 * n] = p;
+                }
+            }
+            __syncthreads();
+#pragma unroll 4
+            for (int n = 0; n < FC_NK; n += 4) {
+                float4 p[RT];
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+                    p[i] = lds4(&w[ty + 16 * i][n]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) {
+                        const float4 v = lds4(&sm.v[n + e][4 * tx + 64 * c]);
+#pragma unroll
+                        for (int i = 0; i < RT; ++i) {
+                            const float pe = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
+                            o[i][c].x = fmaf(pe, v.x, o[i][c].x);
+                            o[i][c].y = fmaf(pe, v.y, o[i][c].y);
+                            o[i][c].z = fmaf(pe, v.z, o[i][c].z);
+                            o[i][c].w = fmaf(pe, v.w, o[i][c].w);
+                        }
+                    }
+            }
+        }
+        const bool whole = it.whole();
+        float *record = P.part + (2 * (int64_t)blockIdx.x + (it.first_part() ? 1 : 0)) * rec;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const int r = ty + 16 * i;
+            float l = sum[i];
+#pragma unroll
+            for (int x = 8; x > 0; x >>= 1)
+                l += __shfl_xor_sync(0xffffffffu, l, x);
+            if (r >= it.rows)
+                continue;
+            const float inv = whole ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+            const int64_t at = (int64_t)(it.row0 + (r >> P.g_log2)) * P.Hq + it.h * G + (r & (G - 1));
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                const float4 v =
+                    make_float4(o[i][c].x * inv, o[i][c].y * inv, o[i][c].z * inv, o[i][c].w * inv);
+                const int col = 4 * tx + 64 * c;
+                if (!whole) {
+                    float2 *dst = reinterpret_cast<float2 *>(record + (int64_t)r * D + col);
+                    dst[0] = make_float2(v.x, v.y);
+                    dst[1] = make_float2(v.z, v.w);
+                } else if constexpr (ES == 4) {
+                    *reinterpret_cast<float4 *>(P.out + (at * D + col) * 4) = v;
+                } else {
+                    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+                    *reinterpret_cast<uint2 *>(P.out + (at * D + col) * 2) = make_uint2(
+                        *reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+                }
+            }
+            if (tx == 0) {
+                if (!whole) {
+                    record[(int64_t)P.rec_rows * D + r] = mx[i];
+                    record[(int64_t)P.rec_rows * (D + 1) + r] = l;
+                } else if (P.lse != nullptr) {
+                    P.lse[at] = l > 0.0f ? (mx[i] + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                }
+            }
+        }
+        if (tid == 0 && !whole && it.first_part())
+            P.desc[blockIdx.x] = ChunkDesc{it.parts(), it.row0, it.h, it.rows};
+    }
+    if (bad)
+        atomicOr(P.status, HKV_DEV_BAD_INDEX);
+}
+
+// =============================================================================
+// Host side
+// =============================================================================
+
+struct ChunkWs {
+    size_t desc, part, total;
+    int rec_rows, ctas;
+};
+
+constexpr int CHUNK_ROWS = 64;  // rows of the largest item
+
+static ChunkWs chunk_ws(const hkv_problem *p, int32_t tokens)
+{
+    ChunkWs w{};
+    const int sms = sm_count();
+    w.ctas = 2 * (sms > 0 ? sms : 148);
+    const int64_t rows = std::min<int64_t>(CHUNK_ROWS, (int64_t)tokens * (p->Hq / p->Hkv));
+    w.rec_rows = (int)((rows + 7) / 8 * 8);
+    const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    w.desc = 256;
+    w.part = w.desc + up((size_t)w.ctas * sizeof(ChunkDesc));
+    w.total = w.part + up((size_t)2 * w.ctas * w.rec_rows * (p->D + 2) * 4);
+    return w;
+}
+
+template <int ES, int D>
+static hkv_status run_chunk(const ChunkP &P, int ctas, cudaStream_t st)
+{
+    // single tokens: items of 16 rows, fewer wasted
+    const bool few = ((int64_t)P.T << P.g_log2) <= 16 * (int64_t)P.B;
+    hkv_status s = few ? launch_dependent(k_chunk_fma<ES, D, 16>, ctas, FC_NT, sizeof(FcSmem<D, 16>), st, P)
+                       : launch_dependent(k_chunk_fma<ES, D, 64>, ctas, FC_NT, sizeof(FcSmem<D, 64>), st, P);
+    if (s != HKV_OK)
+        return s;
+    return launch_dependent(k_chunk_merge<ES, D>, (int64_t)ctas * CMERGE_Y, CMERGE_NT, 0, st, P);
+}
+
+}  // namespace hkv
+
+using namespace hkv;
+
+extern "C" {
+
+hkv_status hkv_chunk_workspace_size(const hkv_problem *prob, int32_t tokens, size_t *bytes)
+{
+    const hkv_status s = check_problem(prob);
+    if (s != HKV_OK)
+        return s;
+    if (tokens < 0 || tokens > HKV_MAX_TOKENS || bytes == nullptr)
+        return HKV_ERR_INVALID_ARG;
+    *bytes = chunk_ws(prob, tokens).total;
+    return HKV_OK;
+}
+
+hkv_status hkv_chunk_attention(const hkv_problem *prob, const void *q, int64_t q_stride, int32_t tokens,
+                               const int32_t *q_start, const int32_t *kv_len, const hkv_pages *pages, void *out,
+                               float *lse, void *ws, size_t ws_bytes, hkv_stream_t stream)
+{
+    hkv_status s = check_problem(prob);
+    if (s != HKV_OK)
+        return s;
+    if (prob->B > HKV_MAX_REQUESTS || tokens < 0 || tokens > HKV_MAX_TOKENS)
+        return HKV_ERR_INVALID_ARG;
+    if ((s = check_pages(pages, prob, true, true)) != HKV_OK)
+        return s;
+    const int es = es_of(prob->dtype), D = prob->D;
+    const auto words = [](const void *p) { return p != nullptr && ptr_aligned(p, 4); };
+    if (prob->B > 0 && (!words(q_start) || !words(kv_len)))
+        return HKV_ERR_INVALID_ARG;
+    if (tokens > 0 && (q == nullptr || out == nullptr || !ptr_aligned(q, 16) || !ptr_aligned(out, 16) ||
+                       q_stride < (int64_t)prob->Hq * D || (q_stride * es) % 16))
+        return HKV_ERR_INVALID_ARG;
+    if (!ptr_aligned(lse, 4))
+        return HKV_ERR_INVALID_ARG;
+    const ChunkWs w = chunk_ws(prob, tokens);
+    if (ws == nullptr || !ptr_aligned(ws, 256) || ws_bytes < w.total)
+        return HKV_ERR_WORKSPACE;
+    if (tokens == 0 || prob->B == 0)
+        return HKV_OK;
+    ChunkP P{};
+    P.q = static_cast<const char *>(q);
+    P.qs = q_stride * es;
+    P.q_start = q_start;
+    P.kv_len = kv_len;
+    P.pages = pages_p(pages, es);
+    P.out = static_cast<char *>(out);
+    P.lse = lse;
+    char *base = static_cast<char *>(ws);
+    P.part = reinterpret_cast<float *>(base + w.part);
+    P.desc = reinterpret_cast<ChunkDesc *>(base + w.desc);
+    P.B = prob->B;
+    P.T = tokens;
+    P.Hq = prob->Hq;
+    P.Hkv = prob->Hkv;
+    P.g_log2 = 31 - __builtin_clz((unsigned)(prob->Hq / prob->Hkv));
+    P.rec_rows = w.rec_rows;
+    P.scale_log2 = (prob->scale > 0.0f ? prob->scale : 1.0f / std::sqrt((float)D)) * 1.4426950408889634f;
+    P.status = reinterpret_cast<uint32_t *>(base);
+    P.wait_ns = g_wait_ns.load();
+    P.withhold = g_withhold.load();
+    const cudaStream_t st = (cudaStream_t)stream;
+    if (prob->dtype == HKV_F32)
+        return D == 128 ? run_chunk<4, 128>(P, w.ctas, st) : run_chunk<4, 64>(P, w.ctas, st);
+    return D == 128 ? run_chunk<2, 128>(P, w.ctas, st) : run_chunk<2, 64>(P, w.ctas, st);
+}
+
+}  // extern "C"

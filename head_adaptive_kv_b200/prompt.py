@@ -1,0 +1,392 @@
+"""Python binding of the prompt side of the cache (``include/hkv_prompt.h``).
+
+Page plans, per-head norms with the position rotation, the attention of a chunk
+of new tokens over the paged cache, and the tiers filled from finished prompts.
+Argument checks and marshalling only, as in ``hkv``; lengths stay on the device.
+"""
+from __future__ import annotations
+
+import ctypes as C
+from contextlib import nullcontext
+from dataclasses import dataclass
+from typing import Optional
+
+import torch
+
+from .hkv import HkvError, Problem, Tier, _check, lib
+
+DEV_PAGES_FULL = 0x40
+MAX_REQUESTS, MAX_TOKENS = 8192, 1 << 22
+
+
+class _Pages(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("stride_p", C.c_int64), ("stride_h", C.c_int64),
+                ("stride_t", C.c_int64), ("pages", C.c_int32), ("page", C.c_int32), ("table", C.c_void_p),
+                ("table_stride", C.c_int64), ("table_cols", C.c_int32)]
+
+
+class _State(C.Structure):
+    _fields_ = [("free", C.c_void_p), ("free_count", C.c_void_p), ("held", C.c_void_p)]
+
+
+class _Chunk(C.Structure):
+    _fields_ = [("tokens", C.c_int32), ("q_start", C.c_void_p), ("kv_len", C.c_void_p), ("pos", C.c_void_p),
+                ("slot", C.c_void_p)]
+
+
+class _Rope(C.Structure):
+    _fields_ = [("inv_freq", C.c_void_p), ("rot", C.c_int32), ("interleaved", C.c_int32), ("mscale", C.c_float)]
+
+
+def _signatures():
+    P, i32, i64, sz, f32 = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t, C.c_float
+    sig = {
+        "hkv_page_plan": [i32, P, P, P, P, P, P, P, P, sz, P],
+        "hkv_page_release": [i32, P, P, P, P, P, sz, P],
+        "hkv_qk_norm_rope": [P, P, i64, P, i64, P, i64, i32, P, P, P, P, P, f32, P, P, P, P, P, sz, P],
+        "hkv_chunk_workspace_size": [P, i32, C.POINTER(C.c_size_t)],
+        "hkv_chunk_attention": [P, P, i64, i32, P, P, P, P, P, P, sz, P],
+        "hkv_fill_tiers": [P, P, P, P, P, P, P, P, P, sz, P],
+    }
+    for name, args in sig.items():
+        f = getattr(lib, name)
+        f.argtypes = args
+        f.restype = C.c_int
+
+
+_signatures()
+
+
+def _p(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _int32(t: torch.Tensor, shape, what: str):
+    if t.dtype != torch.int32:
+        raise TypeError(f"{what} must be int32")
+    _need(t.shape == torch.Size(shape) and t.is_contiguous(), f"{what} must be contiguous of shape {tuple(shape)}")
+
+
+def _together(device: torch.device, *tensors):
+    """Every tensor on `device`."""
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}")
+
+
+def _call(name: str, device: torch.device, stream, *args):
+    """Call `name` on the device of its tensors, with that device's current stream unless one is given."""
+    there = device.type != "cuda" or device.index == torch.cuda.current_device()
+    with nullcontext() if there else torch.cuda.device(device):
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        _check(getattr(lib, name)(*args, stream.cuda_stream), name)
+
+
+class StatusWorkspace:
+    """Workspace of the calls that use only its status word (256 bytes)."""
+
+    def __init__(self, device, nbytes: int = 256):
+        dev = torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.nbytes = int(nbytes)
+        buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=dev)
+        self.tensor = buf[(-buf.data_ptr()) % 256:][:self.nbytes]
+        self.device = self.tensor.device
+        self.ptr = self.tensor.data_ptr()
+        self.init()
+
+    def init(self, stream=None):
+        """Zero the workspace (again after a timeout)."""
+        _call("hkv_workspace_init", self.device, stream, self.ptr, self.nbytes)
+
+    def status(self, stream=None) -> int:
+        """Read and clear the device status word; returns the HKV_DEV_* bits."""
+        flags = C.c_uint32(0)
+        try:
+            _call("hkv_get_status", self.device, stream, self.ptr, C.byref(flags))
+        except HkvError as e:
+            if e.code not in (4, 5):
+                raise
+        return int(flags.value)
+
+
+def status_workspace(device) -> StatusWorkspace:
+    return StatusWorkspace(device)
+
+
+class ChunkWorkspace(StatusWorkspace):
+    """Workspace of ``chunk_attention`` for up to `tokens` rows; serves the other calls too."""
+
+    def __init__(self, prob: Problem, tokens: int, device):
+        n = C.c_size_t(0)
+        dev = torch.device(device)
+        with torch.cuda.device(dev) if dev.type == "cuda" else nullcontext():
+            _check(lib.hkv_chunk_workspace_size(C.byref(prob.c()), int(tokens), C.byref(n)),
+                   "hkv_chunk_workspace_size")
+        super().__init__(dev, n.value)
+
+
+@dataclass
+class Pages:
+    """The page pool: k, v of [pages, Hkv, page, D] (D contiguous, any other strides, the same for both) and the
+    block tables, int32 [B, columns] (rows contiguous; needed by the calls that read tokens back)."""
+
+    k: torch.Tensor
+    v: torch.Tensor
+    table: Optional[torch.Tensor] = None
+
+    def __post_init__(self):
+        k, v, t = self.k, self.v, self.table
+        _need(k.dim() == 4 and k.stride(3) == 1, "pages must be [pages, Hkv, page, D] with D contiguous")
+        _need(v.shape == k.shape and v.stride() == k.stride() and v.dtype == k.dtype,
+              "K and V must share type, shape and strides")
+        _together(k.device, v, t)
+        if t is not None:
+            if t.dtype != torch.int32:
+                raise TypeError("table must be int32")
+            _need(t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1), "table must be [B, columns] with contiguous rows")
+        # the pool and its tables stay where they are: marshalled once
+        self._c = _Pages(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), k.shape[0], k.shape[2],
+                         _p(t), 0 if t is None else max(t.stride(0), t.shape[1]), 0 if t is None else t.shape[1])
+
+    def c(self) -> _Pages:
+        return self._c
+
+    def fits(self, prob: Problem, table: bool = True):
+        k = self.k
+        if k.dtype != prob.dtype:
+            raise TypeError(f"pages of {k.dtype} for a problem of {prob.dtype}")
+        _need(k.shape[1] == prob.Hkv and k.shape[3] == prob.D, "pages must be [pages, Hkv, page, D] of the problem")
+        if table:
+            _need(self.table is not None and self.table.shape[0] == prob.B, "the call needs block tables [B, columns]")
+
+
+@dataclass
+class PageState:
+    """Allocation state: block tables int32 [B, columns], the stack of free pages int32 [pages] with its count [1]
+    (the top is entry count-1), the pages each request holds [B], and the pool's page size and pages."""
+
+    table: torch.Tensor
+    free: torch.Tensor
+    free_count: torch.Tensor
+    held: torch.Tensor
+    page: int
+    pages: int
+
+    def __post_init__(self):
+        B = self.table.shape[0]
+        if self.table.dtype != torch.int32:
+            raise TypeError("table must be int32")
+        _need(self.table.dim() == 2 and (self.table.shape[1] <= 1 or self.table.stride(1) == 1),
+              "table must be [B, columns] with contiguous rows")
+        _int32(self.free, (self.pages,), "free")
+        _int32(self.free_count, (1,), "free_count")
+        _int32(self.held, (B,), "held")
+        _together(self.table.device, self.free, self.free_count, self.held)
+        self._pages = _Pages(None, None, 0, 0, 0, self.pages, self.page, self.table.data_ptr(),
+                             max(self.table.stride(0), self.table.shape[1]), self.table.shape[1])
+        self._c = _State(self.free.data_ptr(), self.free_count.data_ptr(), self.held.data_ptr())
+
+    @staticmethod
+    def allocate(B: int, columns: int, page: int, pages: int, device) -> "PageState":
+        """An empty state: every page free (page 0 is given out first), no request holds any."""
+        i32 = dict(dtype=torch.int32, device=device)
+        return PageState(torch.full((B, columns), -1, **i32), torch.arange(pages - 1, -1, -1, **i32),
+                         torch.full((1,), pages, **i32), torch.zeros(B, **i32), page, pages)
+
+    def _same_pool(self, other: "PageState"):
+        _need(self.table.data_ptr() == other.table.data_ptr() and self.table.shape == other.table.shape and
+              self.table.stride() == other.table.stride() and self.free.data_ptr() == other.free.data_ptr() and
+              (self.page, self.pages) == (other.page, other.pages),
+              "the states before and after must share tables, stack and pool")
+
+
+@dataclass
+class Chunk:
+    """The rows of one step: q_start [B+1], kv_len [B], pos and slot [tokens], all int32."""
+
+    q_start: torch.Tensor
+    kv_len: torch.Tensor
+    pos: torch.Tensor
+    slot: torch.Tensor
+
+    def __post_init__(self):
+        B, T = self.kv_len.shape[0], self.pos.shape[0]
+        _int32(self.kv_len, (B,), "kv_len")
+        _int32(self.q_start, (B + 1,), "q_start")
+        _int32(self.pos, (T,), "pos")
+        _int32(self.slot, (T,), "slot")
+        _together(self.kv_len.device, self.q_start, self.pos, self.slot)
+        self._c = _Chunk(T, self.q_start.data_ptr(), self.kv_len.data_ptr(), self.pos.data_ptr(), self.slot.data_ptr())
+
+    @staticmethod
+    def allocate(B: int, tokens: int, device) -> "Chunk":
+        i32 = dict(dtype=torch.int32, device=device)
+        return Chunk(torch.zeros(B + 1, **i32), torch.zeros(B, **i32), torch.full((tokens,), -1, **i32),
+                     torch.full((tokens,), -1, **i32))
+
+
+@dataclass
+class Rope:
+    """The position rotation: pair i turns by pos * inv_freq[i] (fp64 [rot/2]); mscale multiplies cosine and sine."""
+
+    inv_freq: Optional[torch.Tensor]
+    rot: int
+    interleaved: bool = False
+    mscale: float = 1.0
+
+    def __post_init__(self):
+        if self.rot:
+            _need(self.inv_freq is not None, "inv_freq is missing")
+            if self.inv_freq.dtype != torch.float64:
+                raise TypeError("inv_freq must be float64")
+            _need(self.inv_freq.shape == (self.rot // 2,) and self.inv_freq.is_contiguous(),
+                  "inv_freq must be contiguous [rot/2]")
+        self._c = _Rope(_p(self.inv_freq), int(self.rot), int(bool(self.interleaved)), float(self.mscale))
+
+    @staticmethod
+    def of_base(rot: int, base: float, device, interleaved: bool = False) -> "Rope":
+        """inv_freq[i] = base^(-2 i / rot)."""
+        i = torch.arange(0, rot, 2, dtype=torch.float64)
+        return Rope((base ** (-i / max(rot, 1))).to(device), rot, interleaved)
+
+
+def page_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, state: PageState, after: PageState, chunk: Chunk,
+              ws: StatusWorkspace, granted: Optional[torch.Tensor] = None, stream=None):
+    """Block tables, slot map and positions for new_len[b] tokens behind the ctx_len[b] cached ones of each request
+    (int32 [B]; see hkv_page_plan). `after` receives the state: it shares `state`'s tables and stack, and may be
+    `state` itself. chunk is written; granted: optional int32 [B], the tokens each request was given (0 where it was
+    left out)."""
+    B = state.table.shape[0]
+    _int32(ctx_len, (B,), "ctx_len")
+    _int32(new_len, (B,), "new_len")
+    _need(chunk.kv_len.shape[0] == B, "chunk and state must have the same requests")
+    if granted is not None:
+        _int32(granted, (B,), "granted")
+    if after is not state:
+        state._same_pool(after)
+    dev = state.table.device
+    _together(dev, ctx_len, new_len, chunk.kv_len, granted, ws.tensor, after.held)
+    _call("hkv_page_plan", dev, stream, B, ctx_len.data_ptr(), new_len.data_ptr(), C.byref(state._pages),
+          C.byref(state._c), C.byref(after._c), C.byref(chunk._c), _p(granted), ws.ptr, ws.nbytes)
+
+
+def page_release(done: torch.Tensor, state: PageState, after: PageState, ws: StatusWorkspace, stream=None):
+    """The pages of the requests with done[b] != 0 (int32 [B]) go back on the stack."""
+    B = state.table.shape[0]
+    _int32(done, (B,), "done")
+    if after is not state:
+        state._same_pool(after)
+    dev = state.table.device
+    _together(dev, done, ws.tensor, after.held)
+    _call("hkv_page_release", dev, stream, B, done.data_ptr(), C.byref(state._pages), C.byref(state._c),
+          C.byref(after._c), ws.ptr, ws.nbytes)
+
+
+def _rows(t: torch.Tensor, prob: Problem, tokens: int, heads: int, what: str) -> int:
+    """Row stride of a [tokens, heads, D] tensor with heads and D contiguous."""
+    if t.dtype != prob.dtype:
+        raise TypeError(f"{what} must be of the problem's type")
+    _need(t.shape == (tokens, heads, prob.D), f"{what} must be [tokens, {heads}, {prob.D}]")
+    _need(t.stride(2) == 1 and (heads == 1 or t.stride(1) == prob.D), f"{what}: heads and D must be contiguous")
+    return t.stride(0) if tokens > 1 else max(t.stride(0), heads * prob.D)
+
+
+def _contiguous(t: torch.Tensor, prob: Problem, tokens: int, heads: int, what: str):
+    _rows(t, prob, tokens, heads, what)
+    _need(t.is_contiguous(), f"{what} must be contiguous")
+
+
+def qk_norm_rope(prob: Problem, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor, rope: Rope,
+                 q_out: torch.Tensor, ws: StatusWorkspace, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, k_out: Optional[torch.Tensor] = None,
+                 v_out: Optional[torch.Tensor] = None, pages: Optional[Pages] = None,
+                 slot: Optional[torch.Tensor] = None, stream=None):
+    """Per-head RMS norm (with q_weight and k_weight, [D]; left out without them) and position rotation of the
+    projected rows q [tokens, Hq, D], k and v [tokens, Hkv, D] at positions pos (int32 [tokens], -1 = skipped row).
+    q goes to q_out; k and v to the slots of the pages (pages and slot) or to k_out and v_out, as hkv.append takes
+    them. See hkv_qk_norm_rope."""
+    T = q.shape[0]
+    qs = _rows(q, prob, T, prob.Hq, "q")
+    ks = _rows(k, prob, T, prob.Hkv, "k")
+    vs = _rows(v, prob, T, prob.Hkv, "v")
+    _int32(pos, (T,), "pos")
+    _contiguous(q_out, prob, T, prob.Hq, "q_out")
+    for w in (q_weight, k_weight):
+        if w is not None:
+            if w.dtype != prob.dtype:
+                raise TypeError("norm weights must be of the problem's type")
+            _need(w.shape == (prob.D,) and w.is_contiguous(), "norm weights must be contiguous [D]")
+    if pages is not None:
+        _need(slot is not None and k_out is None and v_out is None, "pages go with slot, and without k_out and v_out")
+        pages.fits(prob, table=False)
+        _int32(slot, (T,), "slot")
+    else:
+        _need(slot is None and k_out is not None and v_out is not None, "give pages and slot, or k_out and v_out")
+        _contiguous(k_out, prob, T, prob.Hkv, "k_out")
+        _contiguous(v_out, prob, T, prob.Hkv, "v_out")
+    dev = q.device
+    _together(dev, k, v, pos, rope.inv_freq, q_out, q_weight, k_weight, k_out, v_out, slot, ws.tensor,
+              None if pages is None else pages.k)
+    _call("hkv_qk_norm_rope", dev, stream, C.byref(prob.c()), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T,
+          pos.data_ptr(), _p(slot), C.byref(rope._c), _p(q_weight), _p(k_weight), float(eps), q_out.data_ptr(),
+          _p(k_out), _p(v_out), None if pages is None else C.byref(pages._c), ws.ptr, ws.nbytes)
+
+
+def chunk_attention(prob: Problem, q: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, pages: Pages,
+                    out: torch.Tensor, ws: ChunkWorkspace, lse: Optional[torch.Tensor] = None, stream=None):
+    """Attention of a chunk of new tokens over the paged cache: rows q_start[b] .. q_start[b+1]-1 of q are the last
+    tokens of request b, whose kv_len[b] tokens (those included) are in the pages; each attends up to its own
+    position. q, out: [tokens, Hq, D] (out contiguous); lse: optional fp32 [tokens, Hq]. See hkv_chunk_attention."""
+    T = q.shape[0]
+    qs = _rows(q, prob, T, prob.Hq, "q")
+    _contiguous(out, prob, T, prob.Hq, "out")
+    _int32(q_start, (prob.B + 1,), "q_start")
+    _int32(kv_len, (prob.B,), "kv_len")
+    pages.fits(prob)
+    if lse is not None:
+        if lse.dtype != torch.float32:
+            raise TypeError("lse must be float32")
+        _need(lse.shape == (T, prob.Hq) and lse.is_contiguous(), "lse must be contiguous [tokens, Hq]")
+    dev = q.device
+    _together(dev, q_start, kv_len, pages.k, out, lse, ws.tensor)
+    _call("hkv_chunk_attention", dev, stream, C.byref(prob.c()), q.data_ptr(), qs, T, q_start.data_ptr(),
+          kv_len.data_ptr(), C.byref(pages._c), out.data_ptr(), _p(lse), ws.ptr, ws.nbytes)
+
+
+def _tier_c(t: Optional[Tier], prob: Problem, what: str):
+    if t is None:
+        return None
+    if t.k.dtype != prob.dtype:
+        raise TypeError(f"{what}: tier of another type than the problem's")
+    _need(t.v is not None and t.v.dtype == prob.dtype, f"{what}: the tier needs V of the problem's type")
+    _need(t.k.shape[0] == prob.B and t.k.shape[1] == prob.Hkv and t.k.shape[3] == prob.D,
+          f"{what} must be [B, Hkv, cap, D] of the problem")
+    _int32(t.len, (prob.units,), f"{what} lengths")
+    return C.byref(t.c())
+
+
+def fill_tiers(prob: Problem, pages: Pages, kv_len: torch.Tensor, dense: Optional[Tier], head: Optional[torch.Tensor],
+               sparse: Optional[Tier], ws: StatusWorkspace, take: Optional[torch.Tensor] = None,
+               dropped: Optional[torch.Tensor] = None, stream=None):
+    """The dense and sparse tiers of finished prompts (all, or those with take[b] != 0), from their pages: what
+    kv_len[b] calls of hkv.append leave, started from empty tiers. head, dropped: int32 [B*Hkv]."""
+    pages.fits(prob)
+    _int32(kv_len, (prob.B,), "kv_len")
+    if take is not None:
+        _int32(take, (prob.B,), "take")
+    for t, what in ((head, "head"), (dropped, "dropped")):
+        if t is not None:
+            _int32(t, (prob.units,), what)
+    dev = pages.k.device
+    tiers = [x for t in (dense, sparse) if t is not None for x in (t.k, t.v, t.len)]
+    _together(dev, kv_len, take, head, dropped, ws.tensor, *tiers)
+    _call("hkv_fill_tiers", dev, stream, C.byref(prob.c()), C.byref(pages._c), kv_len.data_ptr(), _p(take),
+          _tier_c(dense, prob, "dense"), _p(head), _tier_c(sparse, prob, "sparse"), _p(dropped), ws.ptr, ws.nbytes)
