@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 
 #include "hkv_chunk.cuh"
+#include "hkv_chunk_mma.cuh"
 #include "hkv_host.h"
 
 namespace hkv {
@@ -21,21 +22,7 @@ namespace hkv {
 
 constexpr int FC_NT = 256;
 constexpr int FC_NK = 64;
-
-template <int ES>
-__device__ __forceinline__ float4 widen4(const char *p);
-template <>
-__device__ __forceinline__ float4 widen4<4>(const char *p)
-{
-    return *reinterpret_cast<const float4 *>(p);
-}
-template <>
-__device__ __forceinline__ float4 widen4<2>(const char *p)
-{
-    const uint2 w = *reinterpret_cast<const uint2 *>(p);
-    const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
-    return make_float4(a.x, a.y, b.x, b.y);
-}
+constexpr int FC_M = 64;
 
 template <int D, int M>
 struct FcSmem {
@@ -47,7 +34,7 @@ struct FcSmem {
     int ok[FC_NK];  // the tile's keys that are there
 };
 
-template <int ES, int D, int M>
+template <int D, int M>
 __global__ void __launch_bounds__(FC_NT, 2) k_chunk_fma(const __grid_constant__ ChunkP P)
 {
     extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -71,8 +58,8 @@ __global__ void __launch_bounds__(FC_NT, 2) k_chunk_fma(const __grid_constant__ 
             const int r = i / (D / 4), x = i % (D / 4);
             float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < it.rows)
-                val = widen4<ES>(P.q + (it.row0 + (r >> P.g_log2)) * P.qs +
-                                 ((int64_t)(it.h * G + (r & (G - 1))) * D + 4 * x) * ES);
+                val = *reinterpret_cast<const float4 *>(P.q + (it.row0 + (r >> P.g_log2)) * P.qs +
+                                                        ((int64_t)(it.h * G + (r & (G - 1))) * D + 4 * x) * 4);
             *reinterpret_cast<float4 *>(&sm.q[r][4 * x]) = val;
         }
         float mx[RT], sum[RT];
@@ -97,9 +84,9 @@ __global__ void __launch_bounds__(FC_NT, 2) k_chunk_fma(const __grid_constant__ 
                 }
                 float4 kk = make_float4(0.f, 0.f, 0.f, 0.f), vv = kk;
                 if (p >= 0) {
-                    const int64_t at = row_offset(P.pages, p, it.h, key) + 4 * x * ES;
-                    kk = widen4<ES>(P.pages.k + at);
-                    vv = widen4<ES>(P.pages.v + at);
+                    const int64_t at = row_offset(P.pages, p, it.h, key) + 16 * x;
+                    kk = *reinterpret_cast<const float4 *>(P.pages.k + at);
+                    vv = *reinterpret_cast<const float4 *>(P.pages.v + at);
                 }
                 *reinterpret_cast<float4 *>(&sm.k[r][4 * x]) = kk;
                 *reinterpret_cast<float4 *>(&sm.v[r][4 * x]) = vv;
@@ -209,12 +196,8 @@ __global__ void __launch_bounds__(FC_NT, 2) k_chunk_fma(const __grid_constant__ 
                     float2 *dst = reinterpret_cast<float2 *>(record + (int64_t)r * D + col);
                     dst[0] = make_float2(v.x, v.y);
                     dst[1] = make_float2(v.z, v.w);
-                } else if constexpr (ES == 4) {
-                    *reinterpret_cast<float4 *>(P.out + (at * D + col) * 4) = v;
                 } else {
-                    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-                    *reinterpret_cast<uint2 *>(P.out + (at * D + col) * 2) = make_uint2(
-                        *reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+                    *reinterpret_cast<float4 *>(P.out + (at * D + col) * 4) = v;
                 }
             }
             if (tx == 0) {
@@ -242,14 +225,13 @@ struct ChunkWs {
     int rec_rows, ctas;
 };
 
-constexpr int CHUNK_ROWS = 64;  // rows of the largest item
-
 static ChunkWs chunk_ws(const hkv_problem *p, int32_t tokens)
 {
     ChunkWs w{};
-    const int sms = sm_count();
-    w.ctas = 2 * (sms > 0 ? sms : 148);
-    const int64_t rows = std::min<int64_t>(CHUNK_ROWS, (int64_t)tokens * (p->Hq / p->Hkv));
+    const int sms = sm_count() > 0 ? sm_count() : 148;
+    const bool bf = p->dtype == HKV_BF16;
+    w.ctas = bf ? sms : 2 * sms;
+    const int64_t rows = std::min<int64_t>(bf ? CM_M : FC_M, (int64_t)tokens * (p->Hq / p->Hkv));
     w.rec_rows = (int)((rows + 7) / 8 * 8);
     const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     w.desc = 256;
@@ -258,16 +240,65 @@ static ChunkWs chunk_ws(const hkv_problem *p, int32_t tokens)
     return w;
 }
 
-template <int ES, int D>
-static hkv_status run_chunk(const ChunkP &P, int ctas, cudaStream_t st)
+// Tiled maps of the bf16 kernel, boxes of 64 elements (128 bytes, swizzled) by
+// 128 rows: q as [T][Hq][D] in boxes of one KV head's group, K and V as
+// [pages][Hkv][page][D] in boxes of a page (half a page of 256).
+static bool encode_box(CUtensorMap *m, const void *base, int dims, const cuuint64_t *dim, const cuuint64_t *stride,
+                       const cuuint32_t *box)
+{
+    const auto enc = tensor_map_encoder();
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return enc != nullptr &&
+           enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)dims, const_cast<void *>(base), dim, stride, box, ones,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static hkv_status encode_maps(const hkv_problem *p, const ChunkP &A, ChunkMmaP *M)
+{
+    const cuuint64_t D = (cuuint64_t)p->D;
+    const cuuint32_t G = (cuuint32_t)(p->Hq / p->Hkv);
+    const cuuint64_t qd[3] = {D, (cuuint64_t)p->Hq, (cuuint64_t)A.T}, qst[2] = {D * 2, (cuuint64_t)A.qs};
+    const cuuint32_t qb[3] = {64, G, 128 / G};
+    const PagesP &g = A.pages;
+    const cuuint64_t page = 1ull << g.page_log2, pages = (cuuint64_t)std::max(g.pages, 1);
+    const cuuint64_t kd[4] = {D, page, (cuuint64_t)p->Hkv, pages};
+    // the stride of a dimension of one is never used, but has to be valid
+    const cuuint64_t row = (cuuint64_t)g.st, head = p->Hkv > 1 ? (cuuint64_t)g.sh : row;
+    const cuuint64_t kst[3] = {row, head, g.pages > 1 ? (cuuint64_t)g.sp : row};
+    const cuuint32_t kb[4] = {64, (cuuint32_t)std::min<cuuint64_t>(page, CM_NK), 1, 1};
+    // an empty pool has no address: no load reads through its maps
+    const void *k = g.pages > 0 ? (const void *)g.k : (const void *)A.q, *v = g.pages > 0 ? (const void *)g.v : (const void *)A.q;
+    M->none = (int32_t)pages;
+    return encode_box(&M->q, A.q, 3, qd, qst, qb) && encode_box(&M->k, k, 4, kd, kst, kb) &&
+                   encode_box(&M->v, v, 4, kd, kst, kb)
+               ? HKV_OK
+               : HKV_ERR_INVALID_ARG;
+}
+
+template <int D>
+static hkv_status run_mma(const hkv_problem *p, const ChunkP &A, int ctas, cudaStream_t st)
+{
+    ChunkMmaP M{};
+    M.c = A;
+    hkv_status s = encode_maps(p, A, &M);
+    if (s != HKV_OK)
+        return s;
+    if ((s = launch_dependent(k_chunk_mma<D>, ctas, CM_NT, sizeof(CmSmem<D>) + 1024, st, M)) != HKV_OK)
+        return s;
+    return launch_dependent(k_chunk_merge<2, D>, (int64_t)ctas * CMERGE_Y, CMERGE_NT, 0, st, A);
+}
+
+template <int D>
+static hkv_status run_fma(const ChunkP &P, int ctas, cudaStream_t st)
 {
     // single tokens: items of 16 rows, fewer wasted
     const bool few = ((int64_t)P.T << P.g_log2) <= 16 * (int64_t)P.B;
-    hkv_status s = few ? launch_dependent(k_chunk_fma<ES, D, 16>, ctas, FC_NT, sizeof(FcSmem<D, 16>), st, P)
-                       : launch_dependent(k_chunk_fma<ES, D, 64>, ctas, FC_NT, sizeof(FcSmem<D, 64>), st, P);
+    hkv_status s = few ? launch_dependent(k_chunk_fma<D, 16>, ctas, FC_NT, sizeof(FcSmem<D, 16>), st, P)
+                       : launch_dependent(k_chunk_fma<D, FC_M>, ctas, FC_NT, sizeof(FcSmem<D, FC_M>), st, P);
     if (s != HKV_OK)
         return s;
-    return launch_dependent(k_chunk_merge<ES, D>, (int64_t)ctas * CMERGE_Y, CMERGE_NT, 0, st, P);
+    return launch_dependent(k_chunk_merge<4, D>, (int64_t)ctas * CMERGE_Y, CMERGE_NT, 0, st, P);
 }
 
 }  // namespace hkv
@@ -335,8 +366,8 @@ hkv_status hkv_chunk_attention(const hkv_problem *prob, const void *q, int64_t q
     P.withhold = g_withhold.load();
     const cudaStream_t st = (cudaStream_t)stream;
     if (prob->dtype == HKV_F32)
-        return D == 128 ? run_chunk<4, 128>(P, w.ctas, st) : run_chunk<4, 64>(P, w.ctas, st);
-    return D == 128 ? run_chunk<2, 128>(P, w.ctas, st) : run_chunk<2, 64>(P, w.ctas, st);
+        return D == 128 ? run_fma<128>(P, w.ctas, st) : run_fma<64>(P, w.ctas, st);
+    return D == 128 ? run_mma<128>(prob, P, w.ctas, st) : run_mma<64>(prob, P, w.ctas, st);
 }
 
 }  // extern "C"

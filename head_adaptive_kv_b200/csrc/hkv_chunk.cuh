@@ -181,7 +181,7 @@ template <int M, int NK>
 struct ChunkWalk {
     const ChunkP &P;
     const ChunkLine<M, NK> line;
-    const ChunkShare sh;
+    const ChunkShare &sh;  // in shared memory
     ChunkReq r;
     int b, h, t, m;
     int64_t s;
@@ -190,6 +190,7 @@ struct ChunkWalk {
     int j0, j1;      // this CTA's: [j0, j1)
     int rows, row0;  // valid rows, first token row
     int pos0;        // position of row 0's token
+    int limit;       // keys that the last row sees
 
     __device__ __forceinline__ ChunkWalk(const ChunkP &P_, const ChunkShare &sh_)
         : P(P_), line(P_), sh(sh_), b(sh_.b), h(sh_.h), t(sh_.t), m(0), s(sh_.s)
@@ -205,15 +206,15 @@ struct ChunkWalk {
     {
         if (b >= P.B || s >= sh.x1)
             return false;
-        const int on_line = line.tiles(r, t);
-        all = min(on_line, (r.kv + NK - 1) / NK);
+        const int on_line = line.tiles(r, t), tok = t * line.tt, toks = min(line.tt, r.n - tok);
+        rows = toks << P.g_log2;
+        row0 = r.q0 + tok;
+        pos0 = r.kv - r.n + tok;
+        limit = max(0, pos0 + toks);
+        all = min(on_line, (limit + NK - 1) / NK);
         const int64_t p = s + ITEM_COST;
         j0 = (int)max((int64_t)0, min((int64_t)all, sh.x0 - p));
         j1 = (int)max((int64_t)0, min((int64_t)all, sh.x1 - p));
-        const int tok = t * line.tt;
-        rows = min(line.tt, r.n - tok) << P.g_log2;
-        row0 = r.q0 + tok;
-        pos0 = r.kv - r.n + tok;
         end = p + on_line;
         return true;
     }

@@ -1,0 +1,600 @@
+// hkv_chunk_mma.cuh -- the chunk's attention in bf16 on the tensor cores.
+//
+// One CTA per SM, an item of 256 rows in two row tiles of 128, keys in tiles
+// of 128. Scores S_t = Q_t K^T and outputs O_t += P_t V live in tensor memory
+// (two of each fill its 512 columns at D = 128); the weights P_t overwrite S_t
+// there as bf16 and are the product's A operand without touching shared
+// memory. Warps:
+//   0-3, 4-7  softmax of row tile 0, 1: a thread per row reads S, keeps the
+//             row's maximum and sum, writes P; at the item's end reads O
+//   8         loads Q, and K and V tiles page by page (tiled TMA) into a ring
+//   9         issues the matrix instructions
+//   10        zeroes V rows behind a request's last token: their weights are
+//             0, but what lies there may be NaN
+// The matrix instructions of one thread run in order, so S_t of the next key
+// tile may be issued right behind the product that still reads P_t from the
+// same columns, and a tile's softmax runs under the other tile's products.
+//
+// Items of at most 128 rows (single tokens, short chunks) have one row tile;
+// its key tiles then go to the two softmax groups in turn, each with its own
+// O, joined at the item's end: two tiles in flight hide the softmax latency.
+//
+// The row maximum a weight refers to is only moved when a score passes it by
+// 2^8 (weights up to 2^8 are as exact as below 1, and fp32 sums hold them), so
+// O is rarely rescaled.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "hkv_chunk.cuh"
+#include "hkv_tcgen.cuh"
+
+namespace hkv {
+
+constexpr int CM_NT = 384;
+constexpr int CM_M = 256, CM_NK = 128;
+constexpr float CM_GROW = 8.0f;  // log2 of the growth of a score that moves the reference
+
+struct alignas(64) ChunkMmaP {
+    ChunkP c;
+    CUtensorMap q, k, v;
+    int32_t none;  // a page coordinate outside the pool: the load gives zeros
+};
+
+template <int D>
+struct CmSmem {
+    static constexpr int HALVES = D / 64;
+    static constexpr int TILE = 128 * D * 2;  // bytes of 128 rows
+    static constexpr int NST = D == 128 ? 5 : 10;
+    unsigned char q[2][TILE];
+    unsigned char ring[NST][TILE];
+    uint64_t full[NST], empty[NST];
+    uint64_t tail;             // the item's last V tile has landed (its rows behind the end are zeroed next)
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t x_ready, x_done;  // one row tile: group 1's statistics are there / its O has been read
+    uint64_t drained;          // after a failed wait: the matrix instructions issued are done
+    uint32_t tmem;
+    ChunkShare share;
+    unsigned long long red[CM_NT / 32];
+    float xm[128], xl[128];
+};
+
+// Position in a ring of N stages.
+template <int N>
+struct RingAt {
+    int i = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++i == N) {
+            i = 0;
+            phase ^= 1;
+        }
+    }
+    __device__ __forceinline__ void skip(int n)
+    {
+        const int to = i + n;
+        phase ^= (to / N) & 1;
+        i = to % N;
+    }
+};
+
+// The item's last V tile holds rows behind the request's last token that take
+// part in the product (it runs over whole groups of 16 keys).
+__device__ __forceinline__ bool cm_tail(const ChunkWalk<CM_M, CM_NK> &it)
+{
+    return it.j1 == it.all && it.limit == it.r.kv && (it.r.kv & 15) != 0;
+}
+
+// ---- loads (warp 8) ---------------------------------------------------------------
+
+template <int D>
+__device__ __forceinline__ void cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const Ctl &c, int lane)
+{
+    using SM = CmSmem<D>;
+    const ChunkP &A = P.c;
+    const PagesP &G = A.pages;
+    const int rows = min(1 << G.page_log2, CM_NK);         // of a box
+    const int per = CM_NK / rows;                          // boxes of a tile
+    const uint32_t box = (uint32_t)rows * 128 * SM::HALVES;  // bytes of a box over D
+    RingAt<SM::NST> at;
+    uint32_t items = 0, issued = 0;
+    bool bad = false;
+    if (A.withhold)
+        return;
+    for (ChunkWalk<CM_M, CM_NK> it(A, sm.share); it.item(); it.next()) {
+        const int n = it.j1 - it.j0;
+        if (n <= 0)
+            continue;
+        const bool one = it.rows <= 128;
+        // this lane's page of tile j (lanes below `per`)
+        const auto page = [&](int j) {
+            if (lane >= per)
+                return -1;
+            const int key = j * CM_NK + lane * rows;
+            if (key >= it.limit)
+                return -1;
+            const int p = page_of(G, it.b, key);
+            bad = bad || p < 0;
+            return p;
+        };
+        const auto load = [&](const CUtensorMap *map, int j, int p, bool tail) {
+            if (!mbar_await(&sm.empty[at.i], at.phase ^ 1, c))
+                return false;
+            uint64_t *bar = tail ? &sm.tail : &sm.full[at.i];
+            const int boxes = min(per, (it.limit - j * CM_NK + rows - 1) / rows);
+            if (lane == 0)
+                mbar_arrive_expect_tx(bar, boxes * box);
+            __syncwarp();
+            if (lane < boxes) {
+                const int row = (j * CM_NK + lane * rows) & ((1 << G.page_log2) - 1);
+                for (int h = 0; h < SM::HALVES; ++h)
+                    tma_load4(sm.ring[at.i] + h * (CM_NK * 128) + lane * rows * 128, map, h * 64, row, it.h,
+                              p < 0 ? P.none : p, bar);
+            }
+            at.next();
+            ++issued;
+            return true;
+        };
+        int p0 = page(it.j0), p1 = n > 1 ? page(it.j0 + 1) : -1;
+        if (!mbar_await(&sm.q_empty, (items & 1) ^ 1, c))
+            break;
+        if (lane == 0) {
+            const int tiles = one ? 1 : 2, toks = 128 >> A.g_log2;
+            mbar_arrive_expect_tx(&sm.q_full, tiles * SM::TILE);
+            for (int t = 0; t < tiles; ++t)
+                for (int h = 0; h < SM::HALVES; ++h)
+                    tma_load3(sm.q[t] + h * (128 * 128), &P.q, h * 64, it.h << A.g_log2, it.row0 + t * toks,
+                              &sm.q_full);
+        }
+        __syncwarp();
+        ++items;
+        const bool tail = cm_tail(it);
+        const int ahead = one ? 2 : 1;  // key tiles whose scores are formed ahead of a tile's product with V
+        bool ok = load(&P.k, it.j0, p0, false);
+        if (one && n > 1)
+            ok = ok && load(&P.k, it.j0 + 1, p1, false);
+        for (int j = 0; j < n && ok; ++j) {
+            const int p2 = one && j + 2 < n ? page(it.j0 + j + 2) : -1;
+            ok = load(&P.v, it.j0 + j, p0, tail && j == n - 1);
+            if (j + ahead < n)
+                ok = ok && load(&P.k, it.j0 + j + ahead, one ? p2 : p1, false);
+            p0 = p1;
+            p1 = one ? p2 : (j + 2 < n ? page(it.j0 + j + 2) : -1);
+        }
+        if (!ok)
+            break;
+    }
+    if (bad)
+        raise_flag(c, HKV_DEV_BAD_INDEX);
+    if (timed_out(c)) {
+        // let what is on its way land before the CTA ends
+        RingAt<SM::NST> back = at;
+        for (int i = 0; i < SM::NST && (uint32_t)i < issued; ++i) {
+            if (back.i == 0) {
+                back.i = SM::NST;
+                back.phase ^= 1;
+            }
+            --back.i;
+            mbar_let_land(&sm.full[back.i], back.phase);
+        }
+        if (items > 0)
+            mbar_let_land(&sm.q_full, (items - 1) & 1);
+    }
+}
+
+// ---- rows behind the last token (warp 10) --------------------------------------------
+
+template <int D>
+__device__ __forceinline__ void cm_zero_tails(const ChunkMmaP &P, CmSmem<D> &sm, const Ctl &c, int lane)
+{
+    RingAt<CmSmem<D>::NST> at;
+    uint32_t tails = 0;
+    for (ChunkWalk<CM_M, CM_NK> it(P.c, sm.share); it.item(); it.next()) {
+        const int n = it.j1 - it.j0;
+        if (n <= 0)
+            continue;
+        if (cm_tail(it)) {
+            auto last = at;
+            last.skip(2 * n - 1);
+            // the next such tile may be many items away, so this warp is more patient than those it serves
+            if (!mbar_await(&sm.tail, tails & 1, Ctl{c.status, 64 * c.wait_ns}))
+                return;
+            ++tails;
+            const int from = it.r.kv - (it.all - 1) * CM_NK, to = (from + 15) & ~15;
+            for (int i = lane; i < (to - from) * 8 * CmSmem<D>::HALVES; i += 32) {
+                const int half = i / ((to - from) * 8), rest = i - half * (to - from) * 8;
+                *reinterpret_cast<uint4 *>(sm.ring[last.i] + half * (CM_NK * 128) + (from + rest / 8) * 128 +
+                                           (rest % 8) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm.full[last.i]);
+        }
+        at.skip(2 * n);
+    }
+}
+
+// ---- matrix instructions (one thread of warp 9) -----------------------------------------
+
+template <int D>
+__device__ __forceinline__ bool cm_issue(const ChunkMmaP &P, CmSmem<D> &sm, const Ctl &c)
+{
+    using SM = CmSmem<D>;
+    constexpr uint32_t ID_S = mma_idesc(CM_NK, false), ID_O = mma_idesc(D, true);
+    const uint32_t tmem = sm.tmem;
+    RingAt<SM::NST> at;
+    uint32_t items = 0, p_count[2] = {0, 0};
+    const auto scores = [&](int group, int tile, int stage) {
+        const uint32_t q = smem_addr(sm.q[tile]), k = smem_addr(sm.ring[stage]);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+            const uint32_t off = (s / 4) * (128 * 128) + (s % 4) * 32;
+            mma_ss(tmem + group * 128, mma_desc(q + off, 16), mma_desc(k + off, 16), ID_S, s > 0);
+        }
+        mma_commit(&sm.s_full[group]);
+    };
+    const auto product = [&](int group, int stage, int steps, bool first) {
+        const uint32_t v = smem_addr(sm.ring[stage]);
+        for (int s = 0; s < steps; ++s)
+            mma_ts(tmem + 256 + group * 128, tmem + group * 128 + s * 8, mma_desc(v + s * 2048, CM_NK * 128), ID_O,
+                   !(first && s == 0));
+    };
+    const auto weights = [&](int group) {  // P of the group is in tensor memory
+        if (!mbar_await(&sm.p_full[group], p_count[group] & 1, c))
+            return false;
+        ++p_count[group];
+        tc_fence_after();
+        return true;
+    };
+    const auto landed = [&]() { return mbar_await(&sm.full[at.i], at.phase, c); };
+    for (ChunkWalk<CM_M, CM_NK> it(P.c, sm.share); it.item(); it.next()) {
+        const int n = it.j1 - it.j0;
+        if (n <= 0)
+            continue;
+        const bool one = it.rows <= 128;
+        if (!mbar_await(&sm.q_full, items & 1, c))
+            return false;
+        ++items;
+        const auto steps = [&](int j) { return (min(CM_NK, it.limit - (it.j0 + j) * CM_NK) + 15) / 16; };
+        if (!landed())
+            return false;
+        tc_fence_after();
+        scores(0, 0, at.i);
+        if (!one)
+            scores(1, 1, at.i);
+        mma_commit(&sm.empty[at.i]);
+        at.next();
+        if (one && n > 1) {
+            if (!landed())
+                return false;
+            scores(1, 0, at.i);
+            mma_commit(&sm.empty[at.i]);
+            at.next();
+        }
+        if (n <= (one ? 2 : 1))
+            mma_commit(&sm.q_empty);
+        for (int j = 0; j < n; ++j) {
+            if (one) {
+                const int g = j & 1;
+                if (!landed() || !weights(g))
+                    return false;
+                product(g, at.i, steps(j), j < 2);
+                mma_commit(&sm.empty[at.i]);
+                at.next();
+                if (j + 2 >= n) {
+                    mma_commit(&sm.o_full[g]);
+                } else {
+                    if (!landed())
+                        return false;
+                    scores(g, 0, at.i);
+                    mma_commit(&sm.empty[at.i]);
+                    at.next();
+                    if (j + 3 == n)
+                        mma_commit(&sm.q_empty);
+                }
+                continue;
+            }
+            const bool more = j + 1 < n;
+            const int vs = at.i;
+            if (!landed())
+                return false;
+            at.next();
+            const int ks = at.i;
+            if (more) {
+                if (!landed())
+                    return false;
+                at.next();
+            }
+            for (int g = 0; g < 2; ++g) {
+                if (!weights(g))
+                    return false;
+                product(g, vs, steps(j), j == 0);
+                if (more)
+                    scores(g, g, ks);
+                else
+                    mma_commit(&sm.o_full[g]);
+            }
+            mma_commit(&sm.empty[vs]);
+            if (more) {
+                mma_commit(&sm.empty[ks]);
+                if (j + 2 == n)
+                    mma_commit(&sm.q_empty);
+            }
+        }
+    }
+    return true;
+}
+
+// ---- softmax and output (warps 0-7) -----------------------------------------------------
+
+template <int D>
+__device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, const Ctl &c)
+{
+    const ChunkP &A = P.c;
+    const int tid = threadIdx.x, group = tid / 128, row = tid % 128, lane = tid & 31;
+    const uint32_t lanes = (uint32_t)(row & ~31) << 16;  // this warp's quarter of the tensor memory
+    const uint32_t ts = sm.tmem + group * 128 + lanes, to = sm.tmem + 256 + group * 128 + lanes;
+    const float sc = A.scale_log2;
+    const int G = 1 << A.g_log2;
+    const int64_t rec = (int64_t)A.rec_rows * (D + 2);
+    uint32_t s_count = 0, o_count = 0, x_count = 0, o_other = 0;  // phases; o_other: of group 1, seen from 0
+    for (ChunkWalk<CM_M, CM_NK> it(A, sm.share); it.item(); it.next()) {
+        if (!it.mine())
+            continue;
+        const int n = it.j1 - it.j0;
+        const bool one = it.rows <= 128;
+        const int r = one ? row : group * 128 + row;              // row of the item
+        const bool warp_on = (r & ~31) < it.rows;                 // the warp has rows that are there
+        const int seen = min(it.r.kv, it.pos0 + (r >> A.g_log2) + 1);  // keys the row sees
+        const int least = min(it.r.kv, it.pos0 + ((r & ~31) >> A.g_log2) + 1);  // ... and the warp's first row
+        float m = -INFINITY, l = 0.0f;
+        bool begun = false;
+        for (int j = one ? group : 0; j < n; j += one ? 2 : 1) {
+            const int key0 = (it.j0 + j) * CM_NK;
+            // pages of the tile that are not there (a bit per 16 keys)
+            uint32_t holes = 0;
+            if (warp_on) {
+                const int key = key0 + (lane & 7) * 16;
+                holes = __ballot_sync(0xffffffffu, key < it.limit && page_of(A.pages, it.b, key) < 0) & 0xffu;
+            }
+            if (!mbar_await(&sm.s_full[group], s_count & 1, c))
+                return;
+            ++s_count;
+            if (warp_on) {
+                tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    tmem_ld32(ts + 32 * i, s[i]);
+                tmem_wait_ld();
+                if (least - key0 < CM_NK || holes) {
+                    const int cut = seen - key0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * i + e >= cut || ((holes >> (2 * i + e / 16)) & 1))
+                                s[i][e] = 0xff800000u;  // -inf
+                }
+                float top = __uint_as_float(s[0][0]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        top = fmaxf(top, fmaxf(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])));
+                const bool grow = (top - m) * sc > CM_GROW;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float f = grow ? ex2((m - top) * sc) : 1.0f;
+                    if (grow)
+                        m = top;
+                    l *= f;
+                    if (begun) {
+                        // S of this tile was issued behind the product of the last: O is settled
+#pragma unroll
+                        for (int x = 0; x < D; x += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(to + x, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16(to + x, o);
+                        }
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.0f : m * sc;
+                const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(-ref, -ref);
+                float2 sum[2] = {make_float2(l, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float2 x = ffma2(make_float2(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])), sc2, ref2);
+                        x.x = ex2(x.x);
+                        x.y = ex2(x.y);
+                        sum[(e / 2) & 1] = fadd2(sum[(e / 2) & 1], x);
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
+                        w[e / 2] = *reinterpret_cast<const uint32_t *>(&b);
+                    }
+                    tmem_st16(ts + 16 * i, w);
+                }
+                const float2 both = fadd2(sum[0], sum[1]);
+                l = both.x + both.y;
+                tmem_wait_st();
+                tc_fence_before();
+            }
+            begun = true;
+            mbar_arrive(&sm.p_full[group]);
+        }
+        // the item's output (group 1 of a single row tile hands its part to group 0)
+        const bool mine = begun;
+        if (mine) {
+            if (!mbar_await(&sm.o_full[group], o_count & 1, c))
+                return;
+            ++o_count;
+        }
+        if (!one && n > 0)
+            ++o_other;
+        const bool two_parts = one && n > 1;
+        if (two_parts && group == 1) {
+            sm.xm[row] = m;
+            sm.xl[row] = l;
+            mbar_arrive(&sm.x_ready);
+            if (!mbar_await(&sm.x_done, x_count & 1, c))
+                return;
+            ++x_count;
+            continue;
+        }
+        if (one && group == 1)
+            continue;
+        float fa = 1.0f, fb = 0.0f;
+        if (two_parts) {
+            if (!mbar_await(&sm.x_ready, x_count & 1, c) || !mbar_await(&sm.o_full[1], o_other & 1, c))
+                return;
+            ++x_count;
+            ++o_other;
+            const float m1 = sm.xm[row], l1 = sm.xl[row], M = fmaxf(m, m1), base = M == -INFINITY ? 0.0f : M;
+            fa = ex2((m - base) * sc);
+            fb = ex2((m1 - base) * sc);
+            l = l * fa + l1 * fb;
+            m = M;
+        }
+        const bool whole = it.whole();
+        const bool valid = r < it.rows;
+        const int64_t at = ((int64_t)it.row0 + (r >> A.g_log2)) * A.Hq + (it.h << A.g_log2) + (r & (G - 1));
+        float *record = A.part + (2 * (int64_t)blockIdx.x + (it.first_part() ? 1 : 0)) * rec;
+        if (warp_on) {
+            tc_fence_after();
+            if (whole) {
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                fa *= inv;
+                fb *= inv;
+            }
+#pragma unroll
+            for (int x = 0; x < D; x += 32) {
+                uint32_t o[32];
+                if (mine) {
+                    tmem_ld32(to + x, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = l > 0.0f ? __float_as_uint(__uint_as_float(o[e]) * fa) : 0u;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = 0u;
+                }
+                if (two_parts) {
+                    uint32_t o1[32];
+                    tmem_ld32(to + 128 + x, o1);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (l > 0.0f)
+                            o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), fb, __uint_as_float(o[e])));
+                }
+                if (!valid)
+                    continue;
+                if (whole) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(A.out + (at * D + x) * 2);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * i]),
+                                                                           __uint_as_float(o[e + 2 * i + 1]));
+                            w[i] = *reinterpret_cast<const uint32_t *>(&b);
+                        }
+                        dst[e / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+                    float2 *dst = reinterpret_cast<float2 *>(record + (int64_t)r * D + x);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        dst[e / 2] = make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
+                }
+            }
+            tc_fence_before();
+            if (valid) {
+                if (!whole) {
+                    record[(int64_t)A.rec_rows * D + r] = m == -INFINITY ? m : m * sc;
+                    record[(int64_t)A.rec_rows * (D + 1) + r] = l;
+                } else if (A.lse != nullptr) {
+                    A.lse[at] = l > 0.0f ? (m * sc + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                }
+            }
+        }
+        if (two_parts)
+            mbar_arrive(&sm.x_done);
+        if (tid == 0 && !whole && it.first_part())
+            A.desc[blockIdx.x] = ChunkDesc{it.parts(), it.row0, it.h, it.rows};
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(CM_NT, 1) k_chunk_mma(const __grid_constant__ ChunkMmaP P)
+{
+    extern __shared__ unsigned char smem_raw[];
+    auto &sm = *reinterpret_cast<CmSmem<D> *>(smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    allow_dependents();  // only the merge follows, which waits for this kernel's end
+    if (tid == 0) {
+        for (int i = 0; i < CmSmem<D>::NST; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 1);
+        }
+        mbar_init(&sm.tail, 1);
+        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.q_empty, 1);
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(&sm.s_full[g], 1);
+            mbar_init(&sm.p_full[g], 128);
+            mbar_init(&sm.o_full[g], 1);
+        }
+        mbar_init(&sm.x_ready, 128);
+        mbar_init(&sm.x_done, 128);
+        mbar_init(&sm.drained, 1);
+        mbar_fence_init();
+    }
+    if (warp == 9)
+        tmem_alloc(&sm.tmem, 512);
+    wait_prior_grid();
+    const Ctl c{P.c.status, P.c.wait_ns};
+    if (tid == 0)
+        P.c.desc[blockIdx.x].n = 0;
+    tc_fence_before();
+    chunk_share<CM_NT, CM_M, CM_NK>(P.c, sm.red, &sm.share);  // (its barriers publish the set-up above)
+    __syncthreads();
+    tc_fence_after();
+    // the launch's 384 x 168 registers, as 256 x 208 + 128 x 88: a softmax thread holds a row of S
+    if (warp < 8) {
+        regs_take<208>();
+        cm_softmax<D>(P, sm, c);
+    } else {
+        regs_give<88>();
+        if (warp == 8) {
+            cm_load<D>(P, sm, c, lane);
+        } else if (warp == 9) {
+            if (lane == 0 && !cm_issue<D>(P, sm, c)) {
+                mma_commit(&sm.drained);
+                mbar_let_land(&sm.drained, 0);
+            }
+            __syncwarp();
+        } else if (warp == 10) {
+            cm_zero_tails<D>(P, sm, c, lane);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_free(sm.tmem, 512);
+    }
+}
+
+}  // namespace hkv

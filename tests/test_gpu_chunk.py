@@ -342,3 +342,21 @@ def test_prompt_to_decode(dtype):
             want = torch.einsum("hgn,hnd->hgd", s.softmax(-1), vc[b].double()).reshape(Hq, D)
             assert (so.out[b].double() - want).abs().max() <= H.ATOL
     assert ws.status() == 0 and sws.status() == 0
+
+
+def test_waits_that_run_out_end_the_call():
+    """Loads withheld: every wait of the kernel runs out, it returns, the status word says so, and after the workspace is
+    zeroed again the next call is right."""
+    c = Case([(300, 40), (20, 1)], 8, 2, 128, BF, 32, seed=17)
+    hkv.set_wait_limit_ns(2_000_000)
+    hkv.debug_withhold_publish(True)
+    try:
+        c.run()
+        torch.cuda.synchronize()
+    finally:
+        hkv.debug_withhold_publish(False)
+        hkv.set_wait_limit_ns(1_000_000_000)
+    assert c.ws.status() == hkv.DEV_TIMEOUT
+    c.ws.init()
+    c.out.fill_(5.0), c.lse.fill_(5.0)
+    c.run().check()
