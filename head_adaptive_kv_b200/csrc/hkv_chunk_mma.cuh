@@ -8,7 +8,7 @@
 //   0-3, 4-7  softmax of row tile 0, 1: a thread per row reads S, keeps the
 //             row's maximum and sum, writes P; at the item's end reads O
 //   8         loads Q, and K and V tiles page by page (tiled TMA) into a ring
-//   9         issues the matrix instructions
+//   9, 11     issue the matrix instructions of softmax group 0, 1
 //   10        zeroes V rows behind a request's last token: their weights are
 //             0, but what lies there may be NaN
 // The matrix instructions of one thread run in order, so S_t of the next key
@@ -49,11 +49,11 @@ struct CmSmem {
     unsigned char q[2][TILE];
     unsigned char ring[NST][TILE];
     uint64_t full[NST], empty[NST];
-    uint64_t tail;             // the item's last V tile has landed (its rows behind the end are zeroed next)
+    uint64_t tail[NST];        // an item's last V tile has landed (its rows behind the end are zeroed next)
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2], o_full[2];
     uint64_t x_ready, x_done;  // one row tile: group 1's statistics are there / its O has been read
-    uint64_t drained;          // after a failed wait: the matrix instructions issued are done
+    uint64_t drained[2];       // after a failed wait: the matrix instructions issued are done
     uint32_t tmem;
     ChunkShare share;
     unsigned long long red[CM_NT / 32];
@@ -122,7 +122,7 @@ __device__ __forceinline__ void cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const
         const auto load = [&](const CUtensorMap *map, int j, int p, bool tail) {
             if (!mbar_await(&sm.empty[at.i], at.phase ^ 1, c))
                 return false;
-            uint64_t *bar = tail ? &sm.tail : &sm.full[at.i];
+            uint64_t *bar = tail ? &sm.tail[at.i] : &sm.full[at.i];
             const int boxes = min(per, (it.limit - j * CM_NK + rows - 1) / rows);
             if (lane == 0)
                 mbar_arrive_expect_tx(bar, boxes * box);
@@ -190,7 +190,7 @@ template <int D>
 __device__ __forceinline__ void cm_zero_tails(const ChunkMmaP &P, CmSmem<D> &sm, const Ctl &c, int lane)
 {
     RingAt<CmSmem<D>::NST> at;
-    uint32_t tails = 0;
+    uint32_t phases = 0;  // of each stage's tail barrier
     for (ChunkWalk<CM_M, CM_NK> it(P.c, sm.share); it.item(); it.next()) {
         const int n = it.j1 - it.j0;
         if (n <= 0)
@@ -199,9 +199,9 @@ __device__ __forceinline__ void cm_zero_tails(const ChunkMmaP &P, CmSmem<D> &sm,
             auto last = at;
             last.skip(2 * n - 1);
             // the next such tile may be many items away, so this warp is more patient than those it serves
-            if (!mbar_await(&sm.tail, tails & 1, Ctl{c.status, 64 * c.wait_ns}))
+            if (!mbar_await(&sm.tail[last.i], (phases >> last.i) & 1, Ctl{c.status, 64 * c.wait_ns}))
                 return;
-            ++tails;
+            phases ^= 1u << last.i;
             const int from = it.r.kv - (it.all - 1) * CM_NK, to = (from + 15) & ~15;
             for (int i = lane; i < (to - from) * 8 * CmSmem<D>::HALVES; i += 32) {
                 const int half = i / ((to - from) * 8), rest = i - half * (to - from) * 8;
@@ -217,111 +217,148 @@ __device__ __forceinline__ void cm_zero_tails(const ChunkMmaP &P, CmSmem<D> &sm,
     }
 }
 
-// ---- matrix instructions (one thread of warp 9) -----------------------------------------
+// ---- matrix instructions (warps 9 and 11, one per softmax group) --------------------------
+//
+// The warp stays converged and one elected lane issues, so that descriptors
+// live in uniform registers: a single warp issuing for both groups, or code in
+// which one lane runs alone, could not keep the tensor cores fed.
 
 template <int D>
-__device__ __forceinline__ bool cm_issue(const ChunkMmaP &P, CmSmem<D> &sm, const Ctl &c)
+__device__ __forceinline__ bool cm_issue(const ChunkMmaP &P, CmSmem<D> &sm, const Ctl &c, const int g)
 {
     using SM = CmSmem<D>;
     constexpr uint32_t ID_S = mma_idesc(CM_NK, false), ID_O = mma_idesc(D, true);
-    const uint32_t tmem = sm.tmem;
+    const uint32_t ts = sm.tmem + g * 128, to = sm.tmem + 256 + g * 128;
+    const uint32_t ring = mma_low(smem_addr(sm.ring[0]), 0), q0 = mma_low(smem_addr(sm.q[0]), 16);
     RingAt<SM::NST> at;
-    uint32_t items = 0, p_count[2] = {0, 0};
-    const auto scores = [&](int group, int tile, int stage) {
-        const uint32_t q = smem_addr(sm.q[tile]), k = smem_addr(sm.ring[stage]);
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-            const uint32_t off = (s / 4) * (128 * 128) + (s % 4) * 32;
-            mma_ss(tmem + group * 128, mma_desc(q + off, 16), mma_desc(k + off, 16), ID_S, s > 0);
-        }
-        mma_commit(&sm.s_full[group]);
-    };
-    const auto product = [&](int group, int stage, int steps, bool first) {
-        const uint32_t v = smem_addr(sm.ring[stage]);
-        for (int s = 0; s < steps; ++s)
-            mma_ts(tmem + 256 + group * 128, tmem + group * 128 + s * 8, mma_desc(v + s * 2048, CM_NK * 128), ID_O,
-                   !(first && s == 0));
-    };
-    const auto weights = [&](int group) {  // P of the group is in tensor memory
-        if (!mbar_await(&sm.p_full[group], p_count[group] & 1, c))
+    uint32_t items = 0, p_count = 0;
+    const auto landed = [&]() { return mbar_await(&sm.full[at.i], at.phase, c); };
+    // Both warps go past every stage and both free it (a parity wait that
+    // skips phases, or one that a faster warp leaves two phases behind, would
+    // be answered for the wrong one).
+    const auto pass = [&]() {
+        if (!landed())
             return false;
-        ++p_count[group];
+        if (elect_one())
+            mbar_arrive(&sm.empty[at.i]);
+        __syncwarp();
+        at.next();
+        return true;
+    };
+    // S = Q K^T with the present stage's K, which is then free
+    const auto scores = [&](uint32_t q) {
+        const uint32_t k = ring + at.i * (SM::TILE >> 4) + (1u << 16);
+        if (elect_one()) {
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s) {
+                const uint32_t off = (s / 4) * (128 * 128 >> 4) + (s % 4) * 2;
+                mma_ss(ts, q + off, k + off, ID_S, s > 0);
+            }
+            mma_commit(&sm.s_full[g]);
+            mma_commit(&sm.empty[at.i]);
+        }
+        __syncwarp();
+        at.next();
+    };
+    // O (+)= P V with the stage's V over `steps` groups of 16 keys; the stage is then free
+    const auto product = [&](int stage, int steps, bool first, bool last) {
+        const uint32_t v = ring + stage * (SM::TILE >> 4) + ((CM_NK * 128 >> 4) << 16);
+        if (elect_one()) {
+            mma_ts(to, ts, v, ID_O, !first);
+            if (steps == CM_NK / 16) {
+#pragma unroll
+                for (int s = 1; s < CM_NK / 16; ++s)
+                    mma_ts(to, ts + s * 8, v + s * (2048 >> 4), ID_O, true);
+            } else {
+                for (int s = 1; s < steps; ++s)
+                    mma_ts(to, ts + s * 8, v + s * (2048 >> 4), ID_O, true);
+            }
+            if (last)
+                mma_commit(&sm.o_full[g]);
+            mma_commit(&sm.empty[stage]);
+        }
+        __syncwarp();
+    };
+    const auto weights = [&]() {  // P is in tensor memory
+        if (!mbar_await(&sm.p_full[g], p_count & 1, c))
+            return false;
+        ++p_count;
         tc_fence_after();
         return true;
     };
-    const auto landed = [&]() { return mbar_await(&sm.full[at.i], at.phase, c); };
+    // this group's last scores of the item have been issued: Q is free when they are done
+    const auto q_free = [&]() {
+        if (elect_one())
+            mma_commit(&sm.q_empty);
+        __syncwarp();
+    };
     for (ChunkWalk<CM_M, CM_NK> it(P.c, sm.share); it.item(); it.next()) {
         const int n = it.j1 - it.j0;
         if (n <= 0)
             continue;
         const bool one = it.rows <= 128;
+        const auto steps = [&](int j) { return (min(CM_NK, it.limit - (it.j0 + j) * CM_NK) + 15) / 16; };
         if (!mbar_await(&sm.q_full, items & 1, c))
             return false;
         ++items;
-        const auto steps = [&](int j) { return (min(CM_NK, it.limit - (it.j0 + j) * CM_NK) + 15) / 16; };
+        if (one) {
+            // ring: K0 K1 V0 K2 V1 ...; this group has the key tiles of its parity
+            for (int j = 0; j < min(n, 2); ++j) {
+                if (j != g) {
+                    if (!pass())
+                        return false;
+                    continue;
+                }
+                if (!landed())
+                    return false;
+                tc_fence_after();
+                scores(q0);
+            }
+            if (g + 2 >= n)
+                q_free();
+            for (int j = 0; j < n; ++j) {
+                const bool mine = (j & 1) == g;
+                if (!mine) {
+                    if (!pass() || (j + 2 < n && !pass()))
+                        return false;
+                    continue;
+                }
+                if (!landed() || !weights())
+                    return false;
+                product(at.i, steps(j), j < 2, j + 2 >= n);
+                at.next();
+                if (j + 2 < n) {
+                    if (!landed())
+                        return false;
+                    scores(q0);
+                    if (j + 4 >= n)
+                        q_free();
+                }
+            }
+            continue;
+        }
+        // ring: K0 V0 K1 V1 ...; both groups use every tile
+        const uint32_t q = q0 + g * (SM::TILE >> 4);
         if (!landed())
             return false;
         tc_fence_after();
-        scores(0, 0, at.i);
-        if (!one)
-            scores(1, 1, at.i);
-        mma_commit(&sm.empty[at.i]);
-        at.next();
-        if (one && n > 1) {
-            if (!landed())
-                return false;
-            scores(1, 0, at.i);
-            mma_commit(&sm.empty[at.i]);
-            at.next();
-        }
-        if (n <= (one ? 2 : 1))
-            mma_commit(&sm.q_empty);
+        scores(q);
+        if (n == 1)
+            q_free();
         for (int j = 0; j < n; ++j) {
-            if (one) {
-                const int g = j & 1;
-                if (!landed() || !weights(g))
-                    return false;
-                product(g, at.i, steps(j), j < 2);
-                mma_commit(&sm.empty[at.i]);
-                at.next();
-                if (j + 2 >= n) {
-                    mma_commit(&sm.o_full[g]);
-                } else {
-                    if (!landed())
-                        return false;
-                    scores(g, 0, at.i);
-                    mma_commit(&sm.empty[at.i]);
-                    at.next();
-                    if (j + 3 == n)
-                        mma_commit(&sm.q_empty);
-                }
-                continue;
-            }
-            const bool more = j + 1 < n;
             const int vs = at.i;
             if (!landed())
                 return false;
             at.next();
-            const int ks = at.i;
-            if (more) {
-                if (!landed())
-                    return false;
-                at.next();
-            }
-            for (int g = 0; g < 2; ++g) {
-                if (!weights(g))
-                    return false;
-                product(g, vs, steps(j), j == 0);
-                if (more)
-                    scores(g, g, ks);
-                else
-                    mma_commit(&sm.o_full[g]);
-            }
-            mma_commit(&sm.empty[vs]);
-            if (more) {
-                mma_commit(&sm.empty[ks]);
+            if (j + 1 < n && !landed())
+                return false;
+            if (!weights())
+                return false;
+            product(vs, steps(j), j == 0, j + 1 == n);
+            if (j + 1 < n) {
+                scores(q);
                 if (j + 2 == n)
-                    mma_commit(&sm.q_empty);
+                    q_free();
             }
         }
     }
@@ -546,11 +583,11 @@ __global__ void __launch_bounds__(CM_NT, 1) k_chunk_mma(const __grid_constant__ 
     if (tid == 0) {
         for (int i = 0; i < CmSmem<D>::NST; ++i) {
             mbar_init(&sm.full[i], 1);
-            mbar_init(&sm.empty[i], 1);
+            mbar_init(&sm.empty[i], 2);
+            mbar_init(&sm.tail[i], 1);
         }
-        mbar_init(&sm.tail, 1);
         mbar_init(&sm.q_full, 1);
-        mbar_init(&sm.q_empty, 1);
+        mbar_init(&sm.q_empty, 2);
         for (int g = 0; g < 2; ++g) {
             mbar_init(&sm.s_full[g], 1);
             mbar_init(&sm.p_full[g], 128);
@@ -558,7 +595,8 @@ __global__ void __launch_bounds__(CM_NT, 1) k_chunk_mma(const __grid_constant__ 
         }
         mbar_init(&sm.x_ready, 128);
         mbar_init(&sm.x_done, 128);
-        mbar_init(&sm.drained, 1);
+        mbar_init(&sm.drained[0], 1);
+        mbar_init(&sm.drained[1], 1);
         mbar_fence_init();
     }
     if (warp == 9)
@@ -579,14 +617,12 @@ __global__ void __launch_bounds__(CM_NT, 1) k_chunk_mma(const __grid_constant__ 
         regs_give<88>();
         if (warp == 8) {
             cm_load<D>(P, sm, c, lane);
-        } else if (warp == 9) {
-            if (lane == 0 && !cm_issue<D>(P, sm, c)) {
-                mma_commit(&sm.drained);
-                mbar_let_land(&sm.drained, 0);
-            }
-            __syncwarp();
         } else if (warp == 10) {
             cm_zero_tails<D>(P, sm, c, lane);
+        } else if (const int g = warp == 11; !cm_issue<D>(P, sm, c, g)) {
+            if (elect_one())
+                mma_commit(&sm.drained[g]);
+            mbar_let_land(&sm.drained[g], 0);
         }
     }
     tc_fence_before();

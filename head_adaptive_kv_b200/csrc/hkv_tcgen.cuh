@@ -102,32 +102,45 @@ __host__ __device__ constexpr uint32_t mma_idesc(int n, bool b_mn)
 }
 
 // Matrix descriptor of a 128-byte-swizzled tile: rows of 128 bytes in groups of
-// 8 (1024 bytes). lead: bytes between 64-element blocks of the contiguous
-// dimension (N-contiguous tiles wider than 64 elements).
-__device__ __forceinline__ uint64_t mma_desc(uint32_t addr, uint32_t lead)
+// 8 (1024 bytes). `low`: mma_low of its shared-memory address and the bytes
+// between 64-element blocks of the contiguous dimension (N-contiguous tiles
+// wider than 64 elements); the address advances by whole 16 bytes in it.
+constexpr uint32_t MMA_DESC_HIGH = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ uint32_t mma_low(uint32_t addr, uint32_t lead)
 {
-    return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
+    return ((addr & 0x3ffffu) >> 4) | ((lead >> 4) << 16);
 }
 
 // d (+)= A B, both from shared memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc, bool add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+        "r"(a_low), "r"(b_low), "r"(MMA_DESC_HIGH), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
 
 // d (+)= A B, A from tensor memory (two bf16 a column).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_low, uint32_t idesc, bool add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_low), "r"(MMA_DESC_HIGH), "r"(idesc), "r"((uint32_t)add)
         : "memory");
+}
+
+// One lane of a converged warp (the same one each time).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // Arrive on `bar` once all matrix instructions this thread has issued are done.
