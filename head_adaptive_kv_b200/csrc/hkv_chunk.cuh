@@ -60,36 +60,42 @@ __device__ __forceinline__ ChunkReq chunk_request(const ChunkP &P, int b)
     return r;
 }
 
+__host__ __device__ constexpr int log2_of(int x) { return x <= 1 ? 0 : 1 + log2_of(x / 2); }
+
+// (All sizes here are powers of two: shifts, as this stands before every
+// call's first load.)
 template <int M, int NK>
 struct ChunkLine {
-    int tt;  // tokens of an item
+    static constexpr int NKL = log2_of(NK);
+    int ttl;  // log2 of an item's tokens
 
-    __device__ __forceinline__ explicit ChunkLine(const ChunkP &P) : tt(M >> P.g_log2) {}
+    __device__ __forceinline__ explicit ChunkLine(const ChunkP &P) : ttl(log2_of(M) - P.g_log2) {}
 
-    __device__ __forceinline__ int items(const ChunkReq &r) const { return (r.n + tt - 1) / tt; }
+    __device__ __forceinline__ int tokens() const { return 1 << ttl; }
+    __device__ __forceinline__ int items(const ChunkReq &r) const { return (r.n + tokens() - 1) >> ttl; }
 
     // Tiles of item t on the line: all that its last row may see.
     __device__ __forceinline__ int tiles(const ChunkReq &r, int t) const
     {
-        const int ctx = max(0, r.kv - r.n);
-        const int full = (ctx + (t + 1) * tt + NK - 1) / NK;
-        return t == items(r) - 1 ? min(full, (r.kv + NK - 1) / NK) : full;
+        const int full = (int)((max(0, r.kv - r.n) + ((int64_t)(t + 1) << ttl) + NK - 1) >> NKL);
+        return t == items(r) - 1 ? min(full, (int)(((int64_t)r.kv + NK - 1) >> NKL)) : full;
     }
 
     // Line positions of items 0 .. m-1 of one head (m < items): the sum of
-    // tiles(t) = floor((a + t tt) / NK), tt a power of two below or above NK.
+    // tiles(t) = floor((a + (t << ttl)) / NK).
     __device__ __forceinline__ int64_t before(const ChunkReq &r, int m) const
     {
-        const int64_t a = max(0, r.kv - r.n) + tt + NK - 1;
+        const int64_t a = (int64_t)max(0, r.kv - r.n) + tokens() + NK - 1;
         int64_t s;
-        if (tt >= NK) {
-            s = m * (a / NK) + (int64_t)(tt / NK) * m * (m - 1) / 2;
+        if (ttl >= NKL) {
+            s = m * (a >> NKL) + ((((int64_t)m * (m - 1)) >> 1) << (ttl - NKL));
         } else {
-            // floor((a' + t) / k) with a' = floor(a / tt), k = NK / tt, summed by whole runs of k
-            const int64_t k = NK / tt, a1 = a / tt;
-            const auto F = [k](int64_t x) {
-                const int64_t w = x / k;
-                return k * w * (w - 1) / 2 + w * (x - w * k);
+            // floor((a' + t) / k) with a' = floor(a / tokens), k = NK / tokens, summed by whole runs of k
+            const int kl = NKL - ttl;
+            const int64_t a1 = a >> ttl;
+            const auto F = [kl](int64_t x) {
+                const int64_t w = x >> kl;
+                return (((w * (w - 1)) >> 1) << kl) + w * (x - (w << kl));
             };
             s = F(a1 + m) - F(a1);
         }
@@ -103,12 +109,22 @@ struct ChunkLine {
     }
 };
 
-// Where a CTA's share of the line starts and ends.
+// a / b of non-negative numbers, in 32 bits where they fit.
+__device__ __forceinline__ int64_t line_div(int64_t a, int64_t b)
+{
+    if (((a | b) >> 32) == 0)
+        return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
+
+// Where a CTA's share of the line starts and ends: C positions over N CTAs,
+// C / N each and one more for the first C mod N.
 struct ChunkShare {
-    int64_t x0, x1, total;  // positions
-    int64_t s;              // start of the first item
-    int b, h, t;            // the first item
-    int ctas;               // CTAs that share the line
+    int64_t x0, x1;     // positions
+    int64_t each, more; // C / N, C mod N
+    int64_t s;          // start of the first item
+    int b, h, t;        // the first item
+    ChunkReq r;         // its request
 };
 
 // Every thread of the CTA (NT of them) calls this. `red`: NT/32 words.
@@ -116,39 +132,47 @@ template <int NT, int M, int NK>
 __device__ __forceinline__ void chunk_share(const ChunkP &P, unsigned long long *red, ChunkShare *sh)
 {
     const ChunkLine<M, NK> line(P);
-    bool clamped = false;
-    unsigned long long total = 0;
-    for (int b0 = 0; b0 < P.B; b0 += NT) {
+    // the cost of request b0 + this thread, the cost of those before it in the strip, and the strip's
+    const auto strip = [&](int b0, ChunkReq &r, int64_t &cost, unsigned long long &sum) {
         const int b = b0 + threadIdx.x;
-        unsigned long long cost = 0;
+        r = ChunkReq{};
+        cost = 0;
         if (b < P.B) {
-            const ChunkReq r = chunk_request(P, b);
-            clamped = clamped || r.clamped;
-            cost = (unsigned long long)(line.head_cost(r) * P.Hkv);
+            r = chunk_request(P, b);
+            cost = line.head_cost(r) * P.Hkv;
         }
-        total += block_sum_u64<NT>(cost, red);
+        return (int64_t)block_exclusive_scan<NT>((unsigned long long)cost, red, &sum);
+    };
+    ChunkReq r;
+    int64_t cost;
+    unsigned long long sum;
+    int64_t at = strip(0, r, cost, sum), total = (int64_t)sum;
+    bool clamped = r.clamped;
+    for (int b0 = NT; b0 < P.B; b0 += NT) {
+        ChunkReq x;
+        int64_t c;
+        strip(b0, x, c, sum);
+        total += (int64_t)sum;
+        clamped = clamped || x.clamped;
     }
     if (clamped && blockIdx.x == 0)
         atomicOr(P.status, HKV_DEV_LEN_CLAMPED);
-    const int64_t C = (int64_t)total, N = max((int64_t)1, min((int64_t)gridDim.x, C / MIN_SHARE));
-    const bool idle = blockIdx.x >= N;
-    const int64_t x0 = idle ? C : C * blockIdx.x / N, x1 = idle ? C : C * (blockIdx.x + 1) / N;
+    const int64_t N = max((int64_t)1, min((int64_t)gridDim.x, line_div(total, MIN_SHARE)));
+    const int64_t each = line_div(total, N), more = total - each * N, c = blockIdx.x;
+    const int64_t x0 = c >= N ? total : c * each + min(c, more), x1 = c >= N ? total : x0 + each + (c < more ? 1 : 0);
     if (threadIdx.x == 0)
-        *sh = ChunkShare{x0, x1, C, 0, P.B, 0, 0, (int)N};
+        *sh = ChunkShare{x0, x1, each, more, 0, P.B, 0, 0, ChunkReq{}};
     __syncthreads();
-    unsigned long long seen = 0;
-    for (int b0 = 0; b0 < P.B && x0 < x1; b0 += NT) {
-        const int b = b0 + threadIdx.x;
-        unsigned long long cost = 0, sum;
-        ChunkReq r{};
-        if (b < P.B) {
-            r = chunk_request(P, b);
-            cost = (unsigned long long)(line.head_cost(r) * P.Hkv);
-        }
-        const unsigned long long at = seen + block_exclusive_scan<NT>(cost, red, &sum);
-        if ((int64_t)at <= x0 && x0 < (int64_t)(at + cost)) {
-            const int64_t hc = line.head_cost(r), in = x0 - (int64_t)at;
-            const int h = (int)(in / hc);
+    int64_t seen = 0;
+    for (int b0 = 0; x0 < x1; b0 += NT) {
+        if (b0 > 0)
+            at = strip(b0, r, cost, sum);
+        else if (P.B > NT)
+            at = strip(0, r, cost, sum);
+        at += seen;
+        if (at <= x0 && x0 < at + cost) {
+            const int64_t hc = line.head_cost(r), in = x0 - at;
+            const int h = (int)line_div(in, hc);
             const int64_t rest = in - h * hc;
             int lo = 0, hi = line.items(r);  // before(lo) <= rest < before(hi)
             while (hi - lo > 1) {
@@ -158,13 +182,14 @@ __device__ __forceinline__ void chunk_share(const ChunkP &P, unsigned long long 
                 else
                     hi = mid;
             }
-            sh->b = b;
+            sh->b = b0 + (int)threadIdx.x;
             sh->h = h;
             sh->t = lo;
-            sh->s = (int64_t)at + h * hc + line.before(r, lo);
+            sh->s = at + h * hc + line.before(r, lo);
+            sh->r = r;
         }
-        seen += sum;
-        if ((int64_t)seen > x0)
+        seen += (int64_t)sum;
+        if (seen > x0 || b0 + NT >= P.B)
             break;
     }
     __syncthreads();
@@ -173,7 +198,8 @@ __device__ __forceinline__ void chunk_share(const ChunkP &P, unsigned long long 
 // CTA whose share holds position x.
 __device__ __forceinline__ int chunk_owner(const ChunkShare &sh, int64_t x)
 {
-    return (int)(((x + 1) * sh.ctas - 1) / sh.total);
+    const int64_t big = sh.more * (sh.each + 1);  // positions of the CTAs with one more
+    return (int)(x < big ? line_div(x, sh.each + 1) : sh.more + line_div(x - big, sh.each));
 }
 
 // Walks the items of a CTA's share.
@@ -195,10 +221,8 @@ struct ChunkWalk {
     __device__ __forceinline__ ChunkWalk(const ChunkP &P_, const ChunkShare &sh_)
         : P(P_), line(P_), sh(sh_), b(sh_.b), h(sh_.h), t(sh_.t), m(0), s(sh_.s)
     {
-        if (b < P.B) {
-            r = chunk_request(P, b);
-            m = line.items(r);
-        }
+        r = sh.r;
+        m = line.items(r);
     }
 
     // The item at the walk's place into the fields above; false at the end.
@@ -206,7 +230,7 @@ struct ChunkWalk {
     {
         if (b >= P.B || s >= sh.x1)
             return false;
-        const int on_line = line.tiles(r, t), tok = t * line.tt, toks = min(line.tt, r.n - tok);
+        const int on_line = line.tiles(r, t), tok = t << line.ttl, toks = min(line.tokens(), r.n - tok);
         rows = toks << P.g_log2;
         row0 = r.q0 + tok;
         pos0 = r.kv - r.n + tok;

@@ -45,9 +45,10 @@ template <int D>
 struct CmSmem {
     static constexpr int HALVES = D / 64;
     static constexpr int TILE = 128 * D * 2;  // bytes of 128 rows
-    static constexpr int NST = D == 128 ? 5 : 10;
+    static constexpr int NST = D == 128 ? 4 : 8;
     unsigned char q[2][TILE];
     unsigned char ring[NST][TILE];
+    uint4 out[8][256];         // per softmax warp: 32 rows of 128 bytes on their way out
     uint64_t full[NST], empty[NST];
     uint64_t tail[NST];        // an item's last V tile has landed (its rows behind the end are zeroed next)
     uint64_t q_full, q_empty;
@@ -502,7 +503,9 @@ __device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, co
         }
         const bool whole = it.whole();
         const bool valid = r < it.rows;
-        const int64_t at = ((int64_t)it.row0 + (r >> A.g_log2)) * A.Hq + (it.h << A.g_log2) + (r & (G - 1));
+        const auto row_at = [&](int x) {  // row x of the item in out and lse
+            return ((int64_t)it.row0 + (x >> A.g_log2)) * A.Hq + (it.h << A.g_log2) + (x & (G - 1));
+        };
         float *record = A.part + (2 * (int64_t)blockIdx.x + (it.first_part() ? 1 : 0)) * rec;
         if (warp_on) {
             tc_fence_after();
@@ -511,19 +514,18 @@ __device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, co
                 fa *= inv;
                 fb *= inv;
             }
+            const bool any = l > 0.0f;
+            // 32 output columns of this row
+            const auto columns = [&](int x, uint32_t (&o)[32]) {
 #pragma unroll
-            for (int x = 0; x < D; x += 32) {
-                uint32_t o[32];
+                for (int e = 0; e < 32; ++e)
+                    o[e] = 0u;
                 if (mine) {
                     tmem_ld32(to + x, o);
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        o[e] = l > 0.0f ? __float_as_uint(__uint_as_float(o[e]) * fa) : 0u;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        o[e] = 0u;
+                        o[e] = any ? __float_as_uint(__uint_as_float(o[e]) * fa) : 0u;
                 }
                 if (two_parts) {
                     uint32_t o1[32];
@@ -531,29 +533,56 @@ __device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, co
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        if (l > 0.0f)
+                        if (any)
                             o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), fb, __uint_as_float(o[e])));
                 }
-                if (!valid)
-                    continue;
-                if (whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(A.out + (at * D + x) * 2);
+            };
+            // Each thread has a row; memory wants rows from neighbouring lanes. Eight pieces of 16 bytes a row
+            // pass through shared memory, piece p of row y at p ^ (y mod 8): no two lanes of a quarter warp meet
+            // in a bank, on the way in or out.
+            uint4 *stage = sm.out[tid / 32];
+            const int first = r & ~31;  // the warp's first row of the item
+            const auto pass_on = [&](char *base, int64_t stride, bool to_record) {
+                __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t w[4];
+                for (int i = 0; i < 8; ++i) {
+                    const int y = 4 * i + lane / 8, p = lane % 8;
+                    if (first + y < it.rows)
+                        *reinterpret_cast<uint4 *>(base + (to_record ? first + y : row_at(first + y)) * stride +
+                                                   p * 16) = stage[8 * y + (p ^ (y & 7))];
+                }
+                __syncwarp();
+            };
+            if (whole) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * i]),
-                                                                           __uint_as_float(o[e + 2 * i + 1]));
-                            w[i] = *reinterpret_cast<const uint32_t *>(&b);
+                for (int x = 0; x < D; x += 64) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t o[32];
+                        columns(x + 32 * half, o);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * i]),
+                                                                               __uint_as_float(o[e + 2 * i + 1]));
+                                w[i] = *reinterpret_cast<const uint32_t *>(&b);
+                            }
+                            stage[8 * lane + ((4 * half + e / 8) ^ (lane & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
-                        dst[e / 8] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                } else {
-                    float2 *dst = reinterpret_cast<float2 *>(record + (int64_t)r * D + x);
+                    pass_on(A.out + x * 2, D * 2, false);
+                }
+            } else {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        dst[e / 2] = make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
+                for (int x = 0; x < D; x += 32) {
+                    uint32_t o[32];
+                    columns(x, o);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        stage[8 * lane + ((e / 4) ^ (lane & 7))] = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    pass_on(reinterpret_cast<char *>(record + x), D * 4, true);
                 }
             }
             tc_fence_before();
@@ -562,7 +591,7 @@ __device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, co
                     record[(int64_t)A.rec_rows * D + r] = m == -INFINITY ? m : m * sc;
                     record[(int64_t)A.rec_rows * (D + 1) + r] = l;
                 } else if (A.lse != nullptr) {
-                    A.lse[at] = l > 0.0f ? (m * sc + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                    A.lse[row_at(r)] = l > 0.0f ? (m * sc + log2f(l)) * 0.6931471805599453f : -INFINITY;
                 }
             }
         }
@@ -601,6 +630,8 @@ __global__ void __launch_bounds__(CM_NT, 1) k_chunk_mma(const __grid_constant__ 
     }
     if (warp == 9)
         tmem_alloc(&sm.tmem, 512);
+    if (warp == 8 && lane < 3)
+        tma_prefetch_map(lane == 0 ? &P.q : lane == 1 ? &P.k : &P.v);
     wait_prior_grid();
     const Ctl c{P.c.status, P.c.wait_ns};
     if (tid == 0)

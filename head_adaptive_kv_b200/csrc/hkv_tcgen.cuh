@@ -12,16 +12,19 @@ namespace hkv {
 
 __device__ __forceinline__ bool mbar_await(uint64_t *bar, uint32_t parity, const Ctl &c)
 {
-    if (mbar_try_wait(bar, parity))
-        return true;
-    const uint64_t t0 = global_ns();
+    // the clock and the status word are slow to read beside a wait of a
+    // thousand cycles: looked at only once the wait is a long one
+    uint64_t t0 = 0;
     for (uint32_t it = 1;; ++it) {
         if (mbar_try_wait(bar, parity))
             return true;
-        if ((it & 15u) == 0) {
+        if ((it & 1023u) == 0) {
+            const uint64_t now = global_ns();
+            if (t0 == 0)
+                t0 = now;
             if (timed_out(c))
                 return false;
-            if (global_ns() - t0 > c.wait_ns) {
+            if (now - t0 > c.wait_ns) {
                 raise_flag(c, HKV_DEV_TIMEOUT);
                 return false;
             }
@@ -151,6 +154,11 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar)
 }
 
 // ---- tiled TMA loads (no multicast) ---------------------------------------------
+
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 
 __device__ __forceinline__ void tma_load3(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar)
 {

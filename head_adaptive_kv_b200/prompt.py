@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes as C
 from contextlib import nullcontext
 from dataclasses import dataclass
+from functools import lru_cache
 from typing import Optional
 
 import torch
@@ -57,6 +58,10 @@ def _signatures():
 _signatures()
 
 
+# A call's checks and marshalling cost more host time than its launch, so the
+# checks below ask for plain values (sizes, device numbers) and nothing twice.
+
+
 def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -66,26 +71,50 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _int32(t: torch.Tensor, shape, what: str):
-    if t.dtype != torch.int32:
+def _int32(t: torch.Tensor, n: int, what: str):
+    """A contiguous int32 vector of n elements."""
+    if t.dtype is not torch.int32:
         raise TypeError(f"{what} must be int32")
-    _need(t.shape == torch.Size(shape) and t.is_contiguous(), f"{what} must be contiguous of shape {tuple(shape)}")
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous vector of {n} elements")
 
 
-def _together(device: torch.device, *tensors):
-    """Every tensor on `device`."""
+def _together(device: int, *tensors):
+    """Every tensor on `device` (a number, as get_device gives it)."""
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device}")
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensors on different devices ({t.device})")
 
 
-def _call(name: str, device: torch.device, stream, *args):
-    """Call `name` on the device of its tensors, with that device's current stream unless one is given."""
-    there = device.type != "cuda" or device.index == torch.cuda.current_device()
-    with nullcontext() if there else torch.cuda.device(device):
-        if stream is None:
-            stream = torch.cuda.current_stream(device)
-        _check(getattr(lib, name)(*args, stream.cuda_stream), name)
+@lru_cache(maxsize=256)
+def _problem_c(B, Hq, Hkv, D, dtype, scale, p, bmin, bmax, layout):
+    return Problem(B, Hq, Hkv, D, dtype, p, bmin, bmax, scale, layout).c()
+
+
+def _problem(prob: Problem):
+    """The problem's plain values (these calls use neither its inverse temperatures nor its per-unit p)."""
+    return C.byref(_problem_c(prob.B, prob.Hq, prob.Hkv, prob.D, prob.dtype, prob.scale, prob.p, prob.bmin, prob.bmax,
+                              prob.layout))
+
+
+def _call(fn, device: int, stream, *args):
+    """Call `fn` on the device of its tensors, with that device's current stream unless one is given."""
+    if device < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    if device == torch.cuda.current_device():
+        # (the raw handle: a Stream object costs as much as a launch)
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            return _call(fn, device, stream, *args)
+    if code:
+        _check(code, fn.__name__)
+
+
+def _keep(obj, **fields):
+    """Fields of a frozen object: what its tensors were marshalled to."""
+    for name, value in fields.items():
+        object.__setattr__(obj, name, value)
 
 
 class StatusWorkspace:
@@ -98,19 +127,19 @@ class StatusWorkspace:
         self.nbytes = int(nbytes)
         buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=dev)
         self.tensor = buf[(-buf.data_ptr()) % 256:][:self.nbytes]
-        self.device = self.tensor.device
+        self.device = self.tensor.get_device()
         self.ptr = self.tensor.data_ptr()
         self.init()
 
     def init(self, stream=None):
         """Zero the workspace (again after a timeout)."""
-        _call("hkv_workspace_init", self.device, stream, self.ptr, self.nbytes)
+        _call(lib.hkv_workspace_init, self.device, stream, self.ptr, self.nbytes)
 
     def status(self, stream=None) -> int:
         """Read and clear the device status word; returns the HKV_DEV_* bits."""
         flags = C.c_uint32(0)
         try:
-            _call("hkv_get_status", self.device, stream, self.ptr, C.byref(flags))
+            _call(lib.hkv_get_status, self.device, stream, self.ptr, C.byref(flags))
         except HkvError as e:
             if e.code not in (4, 5):
                 raise
@@ -133,7 +162,7 @@ class ChunkWorkspace(StatusWorkspace):
         super().__init__(dev, n.value)
 
 
-@dataclass
+@dataclass(frozen=True, eq=False)
 class Pages:
     """The page pool: k, v of [pages, Hkv, page, D] (D contiguous, any other strides, the same for both) and the
     block tables, int32 [B, columns] (rows contiguous; needed by the calls that read tokens back)."""
@@ -147,28 +176,30 @@ class Pages:
         _need(k.dim() == 4 and k.stride(3) == 1, "pages must be [pages, Hkv, page, D] with D contiguous")
         _need(v.shape == k.shape and v.stride() == k.stride() and v.dtype == k.dtype,
               "K and V must share type, shape and strides")
-        _together(k.device, v, t)
+        _together(k.get_device(), v, t)
         if t is not None:
             if t.dtype != torch.int32:
                 raise TypeError("table must be int32")
             _need(t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1), "table must be [B, columns] with contiguous rows")
-        # the pool and its tables stay where they are: marshalled once
-        self._c = _Pages(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), k.shape[0], k.shape[2],
-                         _p(t), 0 if t is None else max(t.stride(0), t.shape[1]), 0 if t is None else t.shape[1])
+        # the pool and its tables stay where they are: checked and marshalled once
+        c = _Pages(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), k.shape[0], k.shape[2], _p(t),
+                   0 if t is None else max(t.stride(0), t.shape[1]), 0 if t is None else t.shape[1])
+        _keep(self, _c=c, _ref=C.byref(c), _shape=(k.shape[1], k.shape[3], k.dtype), _device=k.get_device(),
+              _rows=None if t is None else t.shape[0])
 
     def c(self) -> _Pages:
         return self._c
 
     def fits(self, prob: Problem, table: bool = True):
-        k = self.k
-        if k.dtype != prob.dtype:
-            raise TypeError(f"pages of {k.dtype} for a problem of {prob.dtype}")
-        _need(k.shape[1] == prob.Hkv and k.shape[3] == prob.D, "pages must be [pages, Hkv, page, D] of the problem")
-        if table:
-            _need(self.table is not None and self.table.shape[0] == prob.B, "the call needs block tables [B, columns]")
+        if self._shape != (prob.Hkv, prob.D, prob.dtype):
+            if self._shape[2] != prob.dtype:
+                raise TypeError(f"pages of {self._shape[2]} for a problem of {prob.dtype}")
+            raise ValueError("pages must be [pages, Hkv, page, D] of the problem")
+        if table and self._rows != prob.B:
+            raise ValueError("the call needs block tables [B, columns]")
 
 
-@dataclass
+@dataclass(frozen=True, eq=False)
 class PageState:
     """Allocation state: block tables int32 [B, columns], the stack of free pages int32 [pages] with its count [1]
     (the top is entry count-1), the pages each request holds [B], and the pool's page size and pages."""
@@ -186,13 +217,15 @@ class PageState:
             raise TypeError("table must be int32")
         _need(self.table.dim() == 2 and (self.table.shape[1] <= 1 or self.table.stride(1) == 1),
               "table must be [B, columns] with contiguous rows")
-        _int32(self.free, (self.pages,), "free")
-        _int32(self.free_count, (1,), "free_count")
-        _int32(self.held, (B,), "held")
-        _together(self.table.device, self.free, self.free_count, self.held)
-        self._pages = _Pages(None, None, 0, 0, 0, self.pages, self.page, self.table.data_ptr(),
-                             max(self.table.stride(0), self.table.shape[1]), self.table.shape[1])
-        self._c = _State(self.free.data_ptr(), self.free_count.data_ptr(), self.held.data_ptr())
+        _int32(self.free, self.pages, "free")
+        _int32(self.free_count, 1, "free_count")
+        _int32(self.held, B, "held")
+        _together(self.table.get_device(), self.free, self.free_count, self.held)
+        t = self.table
+        pages = _Pages(None, None, 0, 0, 0, self.pages, self.page, t.data_ptr(), max(t.stride(0), t.shape[1]), t.shape[1])
+        c = _State(self.free.data_ptr(), self.free_count.data_ptr(), self.held.data_ptr())
+        _keep(self, _pages=pages, _c=c, _pages_ref=C.byref(pages), _ref=C.byref(c), _device=t.get_device(), _rows=B,
+              _pool=(t.data_ptr(), t.shape, t.stride(), self.free.data_ptr(), self.page, self.pages))
 
     @staticmethod
     def allocate(B: int, columns: int, page: int, pages: int, device) -> "PageState":
@@ -202,13 +235,11 @@ class PageState:
                          torch.full((1,), pages, **i32), torch.zeros(B, **i32), page, pages)
 
     def _same_pool(self, other: "PageState"):
-        _need(self.table.data_ptr() == other.table.data_ptr() and self.table.shape == other.table.shape and
-              self.table.stride() == other.table.stride() and self.free.data_ptr() == other.free.data_ptr() and
-              (self.page, self.pages) == (other.page, other.pages),
-              "the states before and after must share tables, stack and pool")
+        if other is not self and (self._pool != other._pool or self._device != other._device):
+            raise ValueError("the states before and after must share tables, stack and pool")
 
 
-@dataclass
+@dataclass(frozen=True, eq=False)
 class Chunk:
     """The rows of one step: q_start [B+1], kv_len [B], pos and slot [tokens], all int32."""
 
@@ -219,12 +250,13 @@ class Chunk:
 
     def __post_init__(self):
         B, T = self.kv_len.shape[0], self.pos.shape[0]
-        _int32(self.kv_len, (B,), "kv_len")
-        _int32(self.q_start, (B + 1,), "q_start")
-        _int32(self.pos, (T,), "pos")
-        _int32(self.slot, (T,), "slot")
-        _together(self.kv_len.device, self.q_start, self.pos, self.slot)
-        self._c = _Chunk(T, self.q_start.data_ptr(), self.kv_len.data_ptr(), self.pos.data_ptr(), self.slot.data_ptr())
+        _int32(self.kv_len, B, "kv_len")
+        _int32(self.q_start, B + 1, "q_start")
+        _int32(self.pos, T, "pos")
+        _int32(self.slot, T, "slot")
+        _together(self.kv_len.get_device(), self.q_start, self.pos, self.slot)
+        c = _Chunk(T, self.q_start.data_ptr(), self.kv_len.data_ptr(), self.pos.data_ptr(), self.slot.data_ptr())
+        _keep(self, _c=c, _ref=C.byref(c), _rows=B, _device=self.kv_len.get_device())
 
     @staticmethod
     def allocate(B: int, tokens: int, device) -> "Chunk":
@@ -233,7 +265,7 @@ class Chunk:
                      torch.full((tokens,), -1, **i32))
 
 
-@dataclass
+@dataclass(frozen=True, eq=False)
 class Rope:
     """The position rotation: pair i turns by pos * inv_freq[i] (fp64 [rot/2]); mscale multiplies cosine and sine."""
 
@@ -249,7 +281,8 @@ class Rope:
                 raise TypeError("inv_freq must be float64")
             _need(self.inv_freq.shape == (self.rot // 2,) and self.inv_freq.is_contiguous(),
                   "inv_freq must be contiguous [rot/2]")
-        self._c = _Rope(_p(self.inv_freq), int(self.rot), int(bool(self.interleaved)), float(self.mscale))
+        c = _Rope(_p(self.inv_freq), int(self.rot), int(bool(self.interleaved)), float(self.mscale))
+        _keep(self, _c=c, _ref=C.byref(c))
 
     @staticmethod
     def of_base(rot: int, base: float, device, interleaved: bool = False) -> "Rope":
@@ -264,44 +297,51 @@ def page_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, state: PageState, af
     (int32 [B]; see hkv_page_plan). `after` receives the state: it shares `state`'s tables and stack, and may be
     `state` itself. chunk is written; granted: optional int32 [B], the tokens each request was given (0 where it was
     left out)."""
-    B = state.table.shape[0]
-    _int32(ctx_len, (B,), "ctx_len")
-    _int32(new_len, (B,), "new_len")
-    _need(chunk.kv_len.shape[0] == B, "chunk and state must have the same requests")
+    B = state._rows
+    _int32(ctx_len, B, "ctx_len")
+    _int32(new_len, B, "new_len")
+    if chunk._rows != B:
+        raise ValueError("chunk and state must have the same requests")
     if granted is not None:
-        _int32(granted, (B,), "granted")
-    if after is not state:
-        state._same_pool(after)
-    dev = state.table.device
-    _together(dev, ctx_len, new_len, chunk.kv_len, granted, ws.tensor, after.held)
-    _call("hkv_page_plan", dev, stream, B, ctx_len.data_ptr(), new_len.data_ptr(), C.byref(state._pages),
-          C.byref(state._c), C.byref(after._c), C.byref(chunk._c), _p(granted), ws.ptr, ws.nbytes)
+        _int32(granted, B, "granted")
+    state._same_pool(after)
+    dev = state._device
+    _together(dev, ctx_len, new_len, granted)
+    if chunk._device != dev or ws.device != dev:
+        raise ValueError("chunk and workspace must be on the state's device")
+    _call(lib.hkv_page_plan, dev, stream, B, ctx_len.data_ptr(), new_len.data_ptr(), state._pages_ref, state._ref,
+          after._ref, chunk._ref, _p(granted), ws.ptr, ws.nbytes)
 
 
 def page_release(done: torch.Tensor, state: PageState, after: PageState, ws: StatusWorkspace, stream=None):
     """The pages of the requests with done[b] != 0 (int32 [B]) go back on the stack."""
-    B = state.table.shape[0]
-    _int32(done, (B,), "done")
-    if after is not state:
-        state._same_pool(after)
-    dev = state.table.device
-    _together(dev, done, ws.tensor, after.held)
-    _call("hkv_page_release", dev, stream, B, done.data_ptr(), C.byref(state._pages), C.byref(state._c),
-          C.byref(after._c), ws.ptr, ws.nbytes)
+    B = state._rows
+    _int32(done, B, "done")
+    state._same_pool(after)
+    dev = state._device
+    _together(dev, done, ws.tensor)
+    _call(lib.hkv_page_release, dev, stream, B, done.data_ptr(), state._pages_ref, state._ref, after._ref, ws.ptr,
+          ws.nbytes)
 
 
-def _rows(t: torch.Tensor, prob: Problem, tokens: int, heads: int, what: str) -> int:
+def _rows(t: torch.Tensor, dtype: torch.dtype, shape: tuple, what: str) -> int:
     """Row stride of a [tokens, heads, D] tensor with heads and D contiguous."""
-    if t.dtype != prob.dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be of the problem's type")
-    _need(t.shape == (tokens, heads, prob.D), f"{what} must be [tokens, {heads}, {prob.D}]")
-    _need(t.stride(2) == 1 and (heads == 1 or t.stride(1) == prob.D), f"{what}: heads and D must be contiguous")
-    return t.stride(0) if tokens > 1 else max(t.stride(0), heads * prob.D)
+    if t.shape != shape:
+        raise ValueError(f"{what} must be {shape}")
+    tokens, heads, D = shape
+    s = t.stride()
+    if s[2] != 1 or (heads > 1 and s[1] != D):
+        raise ValueError(f"{what}: heads and D must be contiguous")
+    return s[0] if tokens > 1 else max(s[0], heads * D)
 
 
-def _contiguous(t: torch.Tensor, prob: Problem, tokens: int, heads: int, what: str):
-    _rows(t, prob, tokens, heads, what)
-    _need(t.is_contiguous(), f"{what} must be contiguous")
+def _contiguous(t: torch.Tensor, dtype: torch.dtype, shape: tuple, what: str):
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous {shape}")
 
 
 def qk_norm_rope(prob: Problem, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor, rope: Rope,
@@ -313,31 +353,33 @@ def qk_norm_rope(prob: Problem, q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
     projected rows q [tokens, Hq, D], k and v [tokens, Hkv, D] at positions pos (int32 [tokens], -1 = skipped row).
     q goes to q_out; k and v to the slots of the pages (pages and slot) or to k_out and v_out, as hkv.append takes
     them. See hkv_qk_norm_rope."""
-    T = q.shape[0]
-    qs = _rows(q, prob, T, prob.Hq, "q")
-    ks = _rows(k, prob, T, prob.Hkv, "k")
-    vs = _rows(v, prob, T, prob.Hkv, "v")
-    _int32(pos, (T,), "pos")
-    _contiguous(q_out, prob, T, prob.Hq, "q_out")
-    for w in (q_weight, k_weight):
-        if w is not None:
-            if w.dtype != prob.dtype:
-                raise TypeError("norm weights must be of the problem's type")
-            _need(w.shape == (prob.D,) and w.is_contiguous(), "norm weights must be contiguous [D]")
+    T, D, dtype = q.shape[0], prob.D, prob.dtype
+    qs = _rows(q, dtype, (T, prob.Hq, D), "q")
+    ks = _rows(k, dtype, (T, prob.Hkv, D), "k")
+    vs = _rows(v, dtype, (T, prob.Hkv, D), "v")
+    _int32(pos, T, "pos")
+    _contiguous(q_out, dtype, (T, prob.Hq, D), "q_out")
+    if q_weight is not None:
+        _contiguous(q_weight, dtype, (D,), "q_weight")
+    if k_weight is not None:
+        _contiguous(k_weight, dtype, (D,), "k_weight")
+    dev = q.get_device()
     if pages is not None:
-        _need(slot is not None and k_out is None and v_out is None, "pages go with slot, and without k_out and v_out")
+        if slot is None or k_out is not None or v_out is not None:
+            raise ValueError("pages go with slot, and without k_out and v_out")
         pages.fits(prob, table=False)
-        _int32(slot, (T,), "slot")
+        _int32(slot, T, "slot")
+        if pages._device != dev:
+            raise ValueError("pages on another device")
     else:
-        _need(slot is None and k_out is not None and v_out is not None, "give pages and slot, or k_out and v_out")
-        _contiguous(k_out, prob, T, prob.Hkv, "k_out")
-        _contiguous(v_out, prob, T, prob.Hkv, "v_out")
-    dev = q.device
-    _together(dev, k, v, pos, rope.inv_freq, q_out, q_weight, k_weight, k_out, v_out, slot, ws.tensor,
-              None if pages is None else pages.k)
-    _call("hkv_qk_norm_rope", dev, stream, C.byref(prob.c()), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T,
-          pos.data_ptr(), _p(slot), C.byref(rope._c), _p(q_weight), _p(k_weight), float(eps), q_out.data_ptr(),
-          _p(k_out), _p(v_out), None if pages is None else C.byref(pages._c), ws.ptr, ws.nbytes)
+        if slot is not None or k_out is None or v_out is None:
+            raise ValueError("give pages and slot, or k_out and v_out")
+        _contiguous(k_out, dtype, (T, prob.Hkv, D), "k_out")
+        _contiguous(v_out, dtype, (T, prob.Hkv, D), "v_out")
+    _together(dev, k, v, pos, rope.inv_freq, q_out, q_weight, k_weight, k_out, v_out, slot, ws.tensor)
+    _call(lib.hkv_qk_norm_rope, dev, stream, _problem(prob), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T,
+          pos.data_ptr(), _p(slot), rope._ref, _p(q_weight), _p(k_weight), eps, q_out.data_ptr(), _p(k_out), _p(v_out),
+          None if pages is None else pages._ref, ws.ptr, ws.nbytes)
 
 
 def chunk_attention(prob: Problem, q: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, pages: Pages,
@@ -346,19 +388,18 @@ def chunk_attention(prob: Problem, q: torch.Tensor, q_start: torch.Tensor, kv_le
     tokens of request b, whose kv_len[b] tokens (those included) are in the pages; each attends up to its own
     position. q, out: [tokens, Hq, D] (out contiguous); lse: optional fp32 [tokens, Hq]. See hkv_chunk_attention."""
     T = q.shape[0]
-    qs = _rows(q, prob, T, prob.Hq, "q")
-    _contiguous(out, prob, T, prob.Hq, "out")
-    _int32(q_start, (prob.B + 1,), "q_start")
-    _int32(kv_len, (prob.B,), "kv_len")
+    shape = (T, prob.Hq, prob.D)
+    qs = _rows(q, prob.dtype, shape, "q")
+    _contiguous(out, prob.dtype, shape, "out")
+    _int32(q_start, prob.B + 1, "q_start")
+    _int32(kv_len, prob.B, "kv_len")
     pages.fits(prob)
     if lse is not None:
-        if lse.dtype != torch.float32:
-            raise TypeError("lse must be float32")
-        _need(lse.shape == (T, prob.Hq) and lse.is_contiguous(), "lse must be contiguous [tokens, Hq]")
-    dev = q.device
-    _together(dev, q_start, kv_len, pages.k, out, lse, ws.tensor)
-    _call("hkv_chunk_attention", dev, stream, C.byref(prob.c()), q.data_ptr(), qs, T, q_start.data_ptr(),
-          kv_len.data_ptr(), C.byref(pages._c), out.data_ptr(), _p(lse), ws.ptr, ws.nbytes)
+        _contiguous(lse, torch.float32, (T, prob.Hq), "lse")
+    dev = pages._device
+    _together(dev, q, q_start, kv_len, out, lse, ws.tensor)
+    _call(lib.hkv_chunk_attention, dev, stream, _problem(prob), q.data_ptr(), qs, T, q_start.data_ptr(),
+          kv_len.data_ptr(), pages._ref, out.data_ptr(), _p(lse), ws.ptr, ws.nbytes)
 
 
 def _tier_c(t: Optional[Tier], prob: Problem, what: str):
@@ -369,7 +410,7 @@ def _tier_c(t: Optional[Tier], prob: Problem, what: str):
     _need(t.v is not None and t.v.dtype == prob.dtype, f"{what}: the tier needs V of the problem's type")
     _need(t.k.shape[0] == prob.B and t.k.shape[1] == prob.Hkv and t.k.shape[3] == prob.D,
           f"{what} must be [B, Hkv, cap, D] of the problem")
-    _int32(t.len, (prob.units,), f"{what} lengths")
+    _int32(t.len, prob.units, f"{what} lengths")
     return C.byref(t.c())
 
 
@@ -379,14 +420,16 @@ def fill_tiers(prob: Problem, pages: Pages, kv_len: torch.Tensor, dense: Optiona
     """The dense and sparse tiers of finished prompts (all, or those with take[b] != 0), from their pages: what
     kv_len[b] calls of hkv.append leave, started from empty tiers. head, dropped: int32 [B*Hkv]."""
     pages.fits(prob)
-    _int32(kv_len, (prob.B,), "kv_len")
+    _int32(kv_len, prob.B, "kv_len")
     if take is not None:
-        _int32(take, (prob.B,), "take")
+        _int32(take, prob.B, "take")
     for t, what in ((head, "head"), (dropped, "dropped")):
         if t is not None:
-            _int32(t, (prob.units,), what)
-    dev = pages.k.device
-    tiers = [x for t in (dense, sparse) if t is not None for x in (t.k, t.v, t.len)]
-    _together(dev, kv_len, take, head, dropped, ws.tensor, *tiers)
-    _call("hkv_fill_tiers", dev, stream, C.byref(prob.c()), C.byref(pages._c), kv_len.data_ptr(), _p(take),
+            _int32(t, prob.units, what)
+    dev = pages._device
+    for t in (dense, sparse):
+        if t is not None:
+            _together(dev, t.k, t.v, t.len)
+    _together(dev, kv_len, take, head, dropped, ws.tensor)
+    _call(lib.hkv_fill_tiers, dev, stream, _problem(prob), pages._ref, kv_len.data_ptr(), _p(take),
           _tier_c(dense, prob, "dense"), _p(head), _tier_c(sparse, prob, "sparse"), _p(dropped), ws.ptr, ws.nbytes)
