@@ -240,6 +240,11 @@ static ChunkWs chunk_ws(const hkv_problem *p, int32_t tokens)
     return w;
 }
 
+static int64_t merge_blocks(const ChunkP &P, int ctas)
+{
+    return (int64_t)ctas * ((P.rec_rows + CMERGE_ROWS - 1) / CMERGE_ROWS);
+}
+
 // Tiled maps of the bf16 kernel, boxes of 64 elements (128 bytes, swizzled) by
 // 128 rows: q as [T][Hq][D] in boxes of one KV head's group, K and V as
 // [pages][Hkv][page][D] in boxes of a page (half a page of 256).
@@ -286,7 +291,7 @@ static hkv_status run_mma(const hkv_problem *p, const ChunkP &A, int ctas, cudaS
         return s;
     if ((s = launch_dependent(k_chunk_mma<D>, ctas, CM_NT, sizeof(CmSmem<D>) + 1024, st, M)) != HKV_OK)
         return s;
-    return launch_dependent(k_chunk_merge<2, D>, (int64_t)ctas * CMERGE_Y, CMERGE_NT, 0, st, A);
+    return launch_dependent(k_chunk_merge<2, D>, merge_blocks(A, ctas), CMERGE_NT, 0, st, A);
 }
 
 template <int D>
@@ -298,7 +303,7 @@ static hkv_status run_fma(const ChunkP &P, int ctas, cudaStream_t st)
                        : launch_dependent(k_chunk_fma<D, FC_M>, ctas, FC_NT, sizeof(FcSmem<D, FC_M>), st, P);
     if (s != HKV_OK)
         return s;
-    return launch_dependent(k_chunk_merge<4, D>, (int64_t)ctas * CMERGE_Y, CMERGE_NT, 0, st, P);
+    return launch_dependent(k_chunk_merge<4, D>, merge_blocks(P, ctas), CMERGE_NT, 0, st, P);
 }
 
 }  // namespace hkv

@@ -275,10 +275,12 @@ struct ChunkWalk {
 };
 
 // Joins the records of items that cross CTAs: blocks (c, y) take the item that
-// starts in CTA c of the attention's grid, a warp per row. Records are taken
-// in line order, so the result does not depend on timing.
+// starts in CTA c of the attention's grid, a warp per row, CMERGE_ROWS rows a
+// block. Lane i reads the statistics of record i (32 at a time), so a row
+// costs two round trips to memory however many parts it has. The order of
+// the sums follows from the number of records alone, not from timing.
 constexpr int CMERGE_NT = 256;
-constexpr int CMERGE_Y = 4;
+constexpr int CMERGE_ROWS = 16;
 
 template <int ES, int D>
 __device__ __forceinline__ void chunk_store(const ChunkP &P, int64_t at, int lane, const float *o, float inv)
@@ -304,29 +306,53 @@ __global__ void __launch_bounds__(CMERGE_NT) k_chunk_merge(const __grid_constant
 {
     constexpr int E = D / 32;
     wait_prior_grid();
-    const int c = blockIdx.x / CMERGE_Y;
-    const int warp = blockIdx.x % CMERGE_Y * (CMERGE_NT / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int blocks = (P.rec_rows + CMERGE_ROWS - 1) / CMERGE_ROWS;
+    const int c = blockIdx.x / blocks, r0 = (blockIdx.x - c * blocks) * CMERGE_ROWS;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int4 d = __ldcg(reinterpret_cast<const int4 *>(P.desc) + c);
     const int n = d.x, G = 1 << P.g_log2;
+    if (n <= 1)
+        return;
     const int64_t rec = (int64_t)P.rec_rows * (D + 2);
-    for (int r = warp; r < (n > 1 ? d.w : 0); r += CMERGE_Y * (CMERGE_NT / 32)) {
+    // the first part is the second record of its CTA, the others are the first of theirs
+    const auto record = [&](int i) { return P.part + (2 * (int64_t)(c + i) + (i == 0 ? 1 : 0)) * rec; };
+    for (int r = r0 + warp; r < min(d.w, r0 + CMERGE_ROWS); r += CMERGE_NT / 32) {
         float M = -INFINITY, L = 0.0f, o[E];
 #pragma unroll
         for (int e = 0; e < E; ++e)
             o[e] = 0.0f;
-        for (int i = 0; i < n; ++i) {
-            // the first part is the second record of its CTA, the others are the first of theirs
-            const float *at = P.part + (2 * (int64_t)(c + i) + (i == 0 ? 1 : 0)) * rec;
-            const float *stats = at + (int64_t)P.rec_rows * D;
-            const float mi = __ldcg(stats + r), li = __ldcg(stats + P.rec_rows + r);
-            if (mi == -INFINITY)
-                continue;
-            const float Mn = fmaxf(M, mi), fa = ex2(M - Mn), fb = ex2(mi - Mn);
-            L = L * fa + li * fb;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            float mi = -INFINITY, li = 0.0f;
+            if (i0 + lane < n) {
+                const float *stats = record(i0 + lane) + (int64_t)P.rec_rows * D + r;
+                mi = __ldcg(stats);
+                li = __ldcg(stats + P.rec_rows);
+            }
+            const float Mn = fmaxf(M, warp_max(mi));
+            const float base = Mn == -INFINITY ? 0.0f : Mn;  // no keys so far: all weights 0
+            const float f = ex2(M - base), w = ex2(mi - base);
+            L = L * f + warp_sum(li * w);
+            M = Mn;
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                o[e] = o[e] * fa + __ldcg(at + (int64_t)r * D + lane * E + e) * fb;
-            M = Mn;
+                o[e] *= f;
+            const int some = min(32, n - i0);
+#pragma unroll 4
+            for (int i = 0; i < some; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, w, i);
+                const float *at = record(i0 + i) + (int64_t)r * D + lane * E;
+                float x[E];
+                if constexpr (E == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(at));
+                    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+                } else {
+                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(at));
+                    x[0] = v.x, x[1] = v.y;
+                }
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    o[e] = fmaf(x[e], wi, o[e]);
+            }
         }
         const int64_t at = ((int64_t)d.y + (r >> P.g_log2)) * P.Hq + d.z * G + (r & (G - 1));
         chunk_store<ES, D>(P, at, lane, o, L > 0.0f ? 1.0f / L : 0.0f);
