@@ -13,7 +13,15 @@
 //             0, but what lies there may be NaN
 // The matrix instructions of one thread run in order, so S_t of the next key
 // tile may be issued right behind the product that still reads P_t from the
-// same columns, and a tile's softmax runs under the other tile's products.
+// same columns, and a tile's softmax runs under the other tile's products. The
+// two groups take turns at their exponentials: left alone they fall into step,
+// share the exponential units and then leave them idle together (8192 tokens
+// behind 8192, Hq 32, Hkv 8, D 128: 1.61 ms without turns, 1.43 with; taking
+// part of the exponentials on the FMA units made it 1.45 to 1.53, scores in
+// half tiles of 64 keys, two in flight, 1.53: narrow products cost as much as
+// wide ones). The weights go out in halves, so that the product with V begins
+// before the last of them. At that size the card is at its power limit (1.64
+// GHz); 1.15 of the 1.38 PFLOP/s that a library product sustains there.
 //
 // Items of at most 128 rows (single tokens, short chunks) have one row tile;
 // its key tiles then go to the two softmax groups in turn, each with its own
@@ -52,7 +60,9 @@ struct CmSmem {
     uint64_t full[NST], empty[NST];
     uint64_t tail[NST];        // an item's last V tile has landed (its rows behind the end are zeroed next)
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], o_full[2];
+    uint64_t p_half[2], p_full[2];  // the weights of the tile's first 64 keys, of all
+    uint64_t turn[2][4];            // a warp's exponentials may begin: the other group's warp beside it is through
     uint64_t x_ready, x_done;  // one row tile: group 1's statistics are there / its O has been read
     uint64_t drained[2];       // after a failed wait: the matrix instructions issued are done
     uint32_t tmem;
@@ -261,30 +271,45 @@ __device__ __forceinline__ bool cm_issue(const ChunkMmaP &P, CmSmem<D> &sm, cons
         __syncwarp();
         at.next();
     };
-    // O (+)= P V with the stage's V over `steps` groups of 16 keys; the stage is then free
+    // O (+)= P V with the stage's V over `steps` groups of 16 keys, the first four as soon as their weights are
+    // there; the stage is then free
     const auto product = [&](int stage, int steps, bool first, bool last) {
         const uint32_t v = ring + stage * (SM::TILE >> 4) + ((CM_NK * 128 >> 4) << 16);
+        const auto some = [&](int from, int to_step) {
+            for (int s = from; s < to_step; ++s)
+                mma_ts(to, ts + s * 8, v + s * (2048 >> 4), ID_O, !(first && s == 0));
+        };
+        if (!mbar_await(&sm.p_half[g], p_count & 1, c))
+            return false;
+        tc_fence_after();
         if (elect_one()) {
-            mma_ts(to, ts, v, ID_O, !first);
-            if (steps == CM_NK / 16) {
+            if (steps >= 4) {
+                mma_ts(to, ts, v, ID_O, !first);
 #pragma unroll
-                for (int s = 1; s < CM_NK / 16; ++s)
+                for (int s = 1; s < 4; ++s)
                     mma_ts(to, ts + s * 8, v + s * (2048 >> 4), ID_O, true);
             } else {
-                for (int s = 1; s < steps; ++s)
+                some(0, steps);
+            }
+        }
+        __syncwarp();
+        if (!mbar_await(&sm.p_full[g], p_count & 1, c))
+            return false;
+        ++p_count;
+        tc_fence_after();
+        if (elect_one()) {
+            if (steps == 8) {
+#pragma unroll
+                for (int s = 4; s < 8; ++s)
                     mma_ts(to, ts + s * 8, v + s * (2048 >> 4), ID_O, true);
+            } else {
+                some(4, steps);
             }
             if (last)
                 mma_commit(&sm.o_full[g]);
             mma_commit(&sm.empty[stage]);
         }
         __syncwarp();
-    };
-    const auto weights = [&]() {  // P is in tensor memory
-        if (!mbar_await(&sm.p_full[g], p_count & 1, c))
-            return false;
-        ++p_count;
-        tc_fence_after();
         return true;
     };
     // this group's last scores of the item have been issued: Q is free when they are done
@@ -324,9 +349,8 @@ __device__ __forceinline__ bool cm_issue(const ChunkMmaP &P, CmSmem<D> &sm, cons
                         return false;
                     continue;
                 }
-                if (!landed() || !weights())
+                if (!landed() || !product(at.i, steps(j), j < 2, j + 2 >= n))
                     return false;
-                product(at.i, steps(j), j < 2, j + 2 >= n);
                 at.next();
                 if (j + 2 < n) {
                     if (!landed())
@@ -353,9 +377,8 @@ __device__ __forceinline__ bool cm_issue(const ChunkMmaP &P, CmSmem<D> &sm, cons
             at.next();
             if (j + 1 < n && !landed())
                 return false;
-            if (!weights())
+            if (!product(vs, steps(j), j == 0, j + 1 == n))
                 return false;
-            product(vs, steps(j), j == 0, j + 1 == n);
             if (j + 1 < n) {
                 scores(q);
                 if (j + 2 == n)
@@ -372,13 +395,13 @@ template <int D>
 __device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, const Ctl &c)
 {
     const ChunkP &A = P.c;
-    const int tid = threadIdx.x, group = tid / 128, row = tid % 128, lane = tid & 31;
+    const int tid = threadIdx.x, group = tid / 128, row = tid % 128, lane = tid & 31, warp = row / 32;
     const uint32_t lanes = (uint32_t)(row & ~31) << 16;  // this warp's quarter of the tensor memory
     const uint32_t ts = sm.tmem + group * 128 + lanes, to = sm.tmem + 256 + group * 128 + lanes;
     const float sc = A.scale_log2;
     const int G = 1 << A.g_log2;
     const int64_t rec = (int64_t)A.rec_rows * (D + 2);
-    uint32_t s_count = 0, o_count = 0, x_count = 0, o_other = 0;  // phases; o_other: of group 1, seen from 0
+    uint32_t s_count = 0, o_count = 0, x_count = 0, o_other = 0, turns = 0;  // phases; o_other: of group 1, seen from 0
     for (ChunkWalk<CM_M, CM_NK> it(A, sm.share); it.item(); it.next()) {
         if (!it.mine())
             continue;
@@ -417,12 +440,16 @@ __device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, co
                             if (32 * i + e >= cut || ((holes >> (2 * i + e / 16)) & 1))
                                 s[i][e] = 0xff800000u;  // -inf
                 }
-                float top = __uint_as_float(s[0][0]);
+                float part[4];  // four chains: one would wait for itself 64 times
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i) {
+                    part[i] = __uint_as_float(s[i][0]);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        top = fmaxf(top, fmaxf(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])));
+                    for (int e = 1; e < 31; e += 2)
+                        part[i] = fmaxf(part[i], fmaxf(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])));
+                    part[i] = fmaxf(part[i], __uint_as_float(s[i][31]));
+                }
+                const float top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
                 const bool grow = (top - m) * sc > CM_GROW;
                 if (__any_sync(0xffffffffu, grow)) {
                     const float f = grow ? ex2((m - top) * sc) : 1.0f;
@@ -446,9 +473,8 @@ __device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, co
                 const float ref = m == -INFINITY ? 0.0f : m * sc;
                 const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(-ref, -ref);
                 float2 sum[2] = {make_float2(l, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t w[16];
+                // weights of columns 32 i .. 32 i + 31 as bf16 pairs
+                const auto weigh = [&](int i, uint32_t *w) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         float2 x = ffma2(make_float2(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])), sc2, ref2);
@@ -458,15 +484,41 @@ __device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, co
                         const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
                         w[e / 2] = *reinterpret_cast<const uint32_t *>(&b);
                     }
-                    tmem_st16(ts + 16 * i, w);
-                }
+                };
+                if (!one && !mbar_await(&sm.turn[group][warp], (turns & 1) ^ (group == 0), c))
+                    return;
+                uint32_t w[32];
+                weigh(0, w);
+                weigh(1, w + 16);
+                tmem_st32(ts, w);
+                weigh(2, w);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sm.p_half[group]);
+                weigh(3, w + 16);
+                if (!one && lane == 0)
+                    mbar_arrive(&sm.turn[group ^ 1][warp]);
+                tmem_st32(ts + 32, w);
                 const float2 both = fadd2(sum[0], sum[1]);
                 l = both.x + both.y;
                 tmem_wait_st();
                 tc_fence_before();
+                __syncwarp();
+            } else {
+                if (!one && !mbar_await(&sm.turn[group][warp], (turns & 1) ^ (group == 0), c))
+                    return;
+                if (lane == 0) {
+                    mbar_arrive(&sm.p_half[group]);
+                    if (!one)
+                        mbar_arrive(&sm.turn[group ^ 1][warp]);
+                }
             }
+            turns += !one;
             begun = true;
-            mbar_arrive(&sm.p_full[group]);
+            if (lane == 0)
+                mbar_arrive(&sm.p_full[group]);
         }
         // the item's output (group 1 of a single row tile hands its part to group 0)
         const bool mine = begun;
@@ -619,7 +671,10 @@ __global__ void __launch_bounds__(CM_NT, 1) k_chunk_mma(const __grid_constant__ 
         mbar_init(&sm.q_empty, 2);
         for (int g = 0; g < 2; ++g) {
             mbar_init(&sm.s_full[g], 1);
-            mbar_init(&sm.p_full[g], 128);
+            mbar_init(&sm.p_half[g], 4);
+            mbar_init(&sm.p_full[g], 4);
+            for (int w = 0; w < 4; ++w)
+                mbar_init(&sm.turn[g][w], 1);
             mbar_init(&sm.o_full[g], 1);
         }
         mbar_init(&sm.x_ready, 128);

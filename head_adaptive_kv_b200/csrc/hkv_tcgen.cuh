@@ -73,6 +73,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32])
         : "r"(addr));
 }
 
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
 // 16 columns of this thread's lane.
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16])
 {
@@ -203,6 +215,28 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b)
     float2 d;
     asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(rd));
     return d;
+}
+
+// 2^x of a pair on the FMA units, x <= 127 (below -127: 0). Cody-Waite
+// reduction to x = n + f, |f| <= 1/2 (adding 1.5 2^23 rounds to the integer n
+// and leaves it in the low bits), a polynomial of degree 5 for 2^f (minimax of
+// the relative error by Remez exchange), and n added to its exponent. Relative
+// error below 2^-22.1, as ex2.approx.
+__device__ __forceinline__ float2 ex2_fma2(float2 x)
+{
+    constexpr float BIG = 12582912.0f;
+    x.x = fmaxf(x.x, -127.0f);
+    x.y = fmaxf(x.y, -127.0f);
+    const float2 t = fadd2(x, make_float2(BIG, BIG));
+    const float2 n = fadd2(t, make_float2(-BIG, -BIG));
+    const float2 f = fadd2(x, make_float2(-n.x, -n.y));
+    float2 p = ffma2(make_float2(0x1.5c08e6p-10f, 0x1.5c08e6p-10f), f, make_float2(0x1.3d0c52p-7f, 0x1.3d0c52p-7f));
+    p = ffma2(p, f, make_float2(0x1.c6b6e4p-5f, 0x1.c6b6e4p-5f));
+    p = ffma2(p, f, make_float2(0x1.ebf918p-3f, 0x1.ebf918p-3f));
+    p = ffma2(p, f, make_float2(0x1.62e428p-1f, 0x1.62e428p-1f));
+    p = ffma2(p, f, make_float2(0x1.000002p+0f, 0x1.000002p+0f));
+    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
 
 }  // namespace hkv
