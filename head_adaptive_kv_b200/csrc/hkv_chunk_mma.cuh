@@ -135,15 +135,21 @@ __device__ __forceinline__ void cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const
                 return false;
             uint64_t *bar = tail ? &sm.tail[at.i] : &sm.full[at.i];
             const int boxes = min(per, (it.limit - j * CM_NK + rows - 1) / rows);
-            if (lane == 0)
+            const bool lead = elect_one();
+            if (lead)
                 mbar_arrive_expect_tx(bar, boxes * box);
-            __syncwarp();
-            if (lane < boxes) {
-                const int row = (j * CM_NK + lane * rows) & ((1 << G.page_log2) - 1);
-                for (int h = 0; h < SM::HALVES; ++h)
-                    tma_load4(sm.ring[at.i] + h * (CM_NK * 128) + lane * rows * 128, map, h * 64, row, it.h,
-                              p < 0 ? P.none : p, bar);
+            const int row = j * CM_NK & ((1 << G.page_log2) - 1);  // a tile begins a page, or its second half
+            unsigned char *dst = sm.ring[at.i];
+            // (one lane issues all boxes: lanes that issue one each are served one after another, and slower)
+            for (int i = 0; i < boxes; ++i, dst += rows * 128) {
+                const int page = __shfl_sync(0xffffffffu, p < 0 ? P.none : p, i);
+                if (lead) {
+                    tma_load4(dst, map, 0, row, it.h, page, bar);
+                    if (D == 128)
+                        tma_load4(dst + CM_NK * 128, map, 64, row, it.h, page, bar);
+                }
             }
+            __syncwarp();
             at.next();
             ++issued;
             return true;
@@ -434,11 +440,15 @@ __device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, co
                 if (least - key0 < CM_NK || holes) {
                     const int cut = seen - key0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 4; ++i) {
+                        const int n_keep = max(0, min(32, cut - 32 * i));
+                        uint32_t keep = n_keep == 32 ? 0xffffffffu : (1u << n_keep) - 1u;
+                        keep &= ~(((holes >> (2 * i)) & 1u) * 0xffffu | ((holes >> (2 * i + 1)) & 1u) * 0xffff0000u);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (32 * i + e >= cut || ((holes >> (2 * i + e / 16)) & 1))
+                            if (!((keep >> e) & 1u))
                                 s[i][e] = 0xff800000u;  // -inf
+                    }
                 }
                 float part[4];  // four chains: one would wait for itself 64 times
 #pragma unroll
@@ -458,7 +468,7 @@ __device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, co
                     l *= f;
                     if (begun) {
                         // S of this tile was issued behind the product of the last: O is settled
-#pragma unroll
+#pragma unroll 1
                         for (int x = 0; x < D; x += 16) {
                             uint32_t o[16];
                             tmem_ld16(to + x, o);
@@ -596,38 +606,43 @@ __device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, co
             const int first = r & ~31;  // the warp's first row of the item
             const auto pass_on = [&](char *base, int64_t stride, bool to_record) {
                 __syncwarp();
+                const int rows = min(32, it.rows - first);
+#pragma unroll 1
+                for (int y = lane / 8; y < rows; y += 16) {
+                    const int p = lane % 8;
+                    // four rows at once: the loads of shared memory are on their way together
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int y = 4 * i + lane / 8, p = lane % 8;
-                    if (first + y < it.rows)
-                        *reinterpret_cast<uint4 *>(base + (to_record ? first + y : row_at(first + y)) * stride +
-                                                   p * 16) = stage[8 * y + (p ^ (y & 7))];
+                    for (int i = 0; i < 16; i += 4)
+                        if (y + i < rows)
+                            *reinterpret_cast<uint4 *>(
+                                base + (to_record ? first + y + i : row_at(first + y + i)) * stride + p * 16) =
+                                stage[8 * (y + i) + (p ^ ((y + i) & 7))];
                 }
                 __syncwarp();
             };
+            // (loops, not copies: code that runs once an item comes from far away each time)
             if (whole) {
+#pragma unroll 1
+                for (int x = 0; x < D; x += 32) {
+                    uint32_t o[32];
+                    columns(x, o);
+                    const int half = x & 32 ? 4 : 0;
 #pragma unroll
-                for (int x = 0; x < D; x += 64) {
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t w[4];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t o[32];
-                        columns(x + 32 * half, o);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * i]),
-                                                                               __uint_as_float(o[e + 2 * i + 1]));
-                                w[i] = *reinterpret_cast<const uint32_t *>(&b);
-                            }
-                            stage[8 * lane + ((4 * half + e / 8) ^ (lane & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int i = 0; i < 4; ++i) {
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * i]),
+                                                                           __uint_as_float(o[e + 2 * i + 1]));
+                            w[i] = *reinterpret_cast<const uint32_t *>(&b);
                         }
+                        stage[8 * lane + ((half + e / 8) ^ (lane & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    pass_on(A.out + x * 2, D * 2, false);
+                    if (half)
+                        pass_on(A.out + (x - 32) * 2, D * 2, false);
                 }
             } else {
-#pragma unroll
+#pragma unroll 1
                 for (int x = 0; x < D; x += 32) {
                     uint32_t o[32];
                     columns(x, o);
