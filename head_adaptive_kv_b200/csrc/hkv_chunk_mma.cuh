@@ -7,10 +7,8 @@
 // memory. Warps:
 //   0-3, 4-7  softmax of row tile 0, 1: a thread per row reads S, keeps the
 //             row's maximum and sum, writes P; at the item's end reads O
-//   8         loads Q, and K and V tiles page by page (tiled TMA) into a ring
+//   8, 10     load Q, and K and V tiles page by page (tiled TMA) into a ring
 //   9, 11     issue the matrix instructions of softmax group 0, 1
-//   10        zeroes V rows behind a request's last token: their weights are
-//             0, but what lies there may be NaN
 // The matrix instructions of one thread run in order, so S_t of the next key
 // tile may be issued right behind the product that still reads P_t from the
 // same columns, and a tile's softmax runs under the other tile's products. The
@@ -58,7 +56,6 @@ struct CmSmem {
     unsigned char ring[NST][TILE];
     uint4 out[8][256];         // per softmax warp: 32 rows of 128 bytes on their way out
     uint64_t full[NST], empty[NST];
-    uint64_t tail[NST];        // an item's last V tile has landed (its rows behind the end are zeroed next)
     uint64_t q_full, q_empty;
     uint64_t s_full[2], o_full[2];
     uint64_t p_half[2], p_full[2];  // the weights of the tile's first 64 keys, of all
@@ -83,32 +80,31 @@ struct RingAt {
             phase ^= 1;
         }
     }
-    __device__ __forceinline__ void skip(int n)
-    {
-        const int to = i + n;
-        phase ^= (to / N) & 1;
-        i = to % N;
-    }
 };
 
 // The item's last V tile holds rows behind the request's last token that take
-// part in the product (it runs over whole groups of 16 keys).
+// part in the product (it runs over whole groups of 16 keys): their weights
+// are 0, but what lies there may be NaN.
 __device__ __forceinline__ bool cm_tail(const ChunkWalk<CM_M, CM_NK> &it)
 {
     return it.j1 == it.all && it.limit == it.r.kv && (it.r.kv & 15) != 0;
 }
 
-// ---- loads (warp 8) ---------------------------------------------------------------
+// ---- loads (warps 8 and 10) ---------------------------------------------------------------
+
+//
+// A tile's boxes (a page's rows by 64 columns) are issued by two warps in
+// turn: a small box costs its issuer about as much as a large one.
 
 template <int D>
-__device__ __forceinline__ void cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const Ctl &c, int lane)
+__device__ __forceinline__ void cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const Ctl &c, int lane, const int w)
 {
     using SM = CmSmem<D>;
     const ChunkP &A = P.c;
     const PagesP &G = A.pages;
     const int rows = min(1 << G.page_log2, CM_NK);         // of a box
     const int per = CM_NK / rows;                          // boxes of a tile
-    const uint32_t box = (uint32_t)rows * 128 * SM::HALVES;  // bytes of a box over D
+    const uint32_t box = (uint32_t)rows * 128;             // bytes of a box
     RingAt<SM::NST> at;
     uint32_t items = 0, issued = 0;
     bool bad = false;
@@ -127,27 +123,25 @@ __device__ __forceinline__ void cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const
             if (key >= it.limit)
                 return -1;
             const int p = page_of(G, it.b, key);
-            bad = bad || p < 0;
+            bad = bad || (p < 0 && w == 0);
             return p;
         };
-        const auto load = [&](const CUtensorMap *map, int j, int p, bool tail) {
+        const auto load = [&](const CUtensorMap *map, int j, int p) {
             if (!mbar_await(&sm.empty[at.i], at.phase ^ 1, c))
                 return false;
-            uint64_t *bar = tail ? &sm.tail[at.i] : &sm.full[at.i];
+            uint64_t *bar = &sm.full[at.i];
             const int boxes = min(per, (it.limit - j * CM_NK + rows - 1) / rows);
             const bool lead = elect_one();
+            // box i of columns 64 h is this warp's when i HALVES + h is of its parity
             if (lead)
-                mbar_arrive_expect_tx(bar, boxes * box);
+                mbar_arrive_expect_tx(bar, (D == 128 ? boxes : (boxes + 1 - w) / 2) * box);
             const int row = j * CM_NK & ((1 << G.page_log2) - 1);  // a tile begins a page, or its second half
-            unsigned char *dst = sm.ring[at.i];
-            // (one lane issues all boxes: lanes that issue one each are served one after another, and slower)
-            for (int i = 0; i < boxes; ++i, dst += rows * 128) {
+            unsigned char *dst = sm.ring[at.i] + (D == 128 ? w * (CM_NK * 128) : 0);
+            // (one lane issues all its boxes: lanes that issue one each are served one after another, and slower)
+            for (int i = D == 128 ? 0 : w; i < boxes; i += D == 128 ? 1 : 2) {
                 const int page = __shfl_sync(0xffffffffu, p < 0 ? P.none : p, i);
-                if (lead) {
-                    tma_load4(dst, map, 0, row, it.h, page, bar);
-                    if (D == 128)
-                        tma_load4(dst + CM_NK * 128, map, 64, row, it.h, page, bar);
-                }
+                if (lead)
+                    tma_load4(dst + i * rows * 128, map, D == 128 ? 64 * w : 0, row, it.h, page, bar);
             }
             __syncwarp();
             at.next();
@@ -157,26 +151,24 @@ __device__ __forceinline__ void cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const
         int p0 = page(it.j0), p1 = n > 1 ? page(it.j0 + 1) : -1;
         if (!mbar_await(&sm.q_empty, (items & 1) ^ 1, c))
             break;
-        if (lane == 0) {
+        if (elect_one()) {
             const int tiles = one ? 1 : 2, toks = 128 >> A.g_log2;
-            mbar_arrive_expect_tx(&sm.q_full, tiles * SM::TILE);
-            for (int t = 0; t < tiles; ++t)
-                for (int h = 0; h < SM::HALVES; ++h)
-                    tma_load3(sm.q[t] + h * (128 * 128), &P.q, h * 64, it.h << A.g_log2, it.row0 + t * toks,
-                              &sm.q_full);
+            mbar_arrive_expect_tx(&sm.q_full, D == 128 || w == 0 ? tiles * (128 * 128) : 0);
+            if (D == 128 || w == 0)
+                for (int t = 0; t < tiles; ++t)
+                    tma_load3(sm.q[t] + w * (128 * 128), &P.q, 64 * w, it.h << A.g_log2, it.row0 + t * toks, &sm.q_full);
         }
         __syncwarp();
         ++items;
-        const bool tail = cm_tail(it);
         const int ahead = one ? 2 : 1;  // key tiles whose scores are formed ahead of a tile's product with V
-        bool ok = load(&P.k, it.j0, p0, false);
+        bool ok = load(&P.k, it.j0, p0);
         if (one && n > 1)
-            ok = ok && load(&P.k, it.j0 + 1, p1, false);
+            ok = ok && load(&P.k, it.j0 + 1, p1);
         for (int j = 0; j < n && ok; ++j) {
             const int p2 = one && j + 2 < n ? page(it.j0 + j + 2) : -1;
-            ok = load(&P.v, it.j0 + j, p0, tail && j == n - 1);
+            ok = load(&P.v, it.j0 + j, p0);
             if (j + ahead < n)
-                ok = ok && load(&P.k, it.j0 + j + ahead, one ? p2 : p1, false);
+                ok = ok && load(&P.k, it.j0 + j + ahead, one ? p2 : p1);
             p0 = p1;
             p1 = one ? p2 : (j + 2 < n ? page(it.j0 + j + 2) : -1);
         }
@@ -198,39 +190,6 @@ __device__ __forceinline__ void cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const
         }
         if (items > 0)
             mbar_let_land(&sm.q_full, (items - 1) & 1);
-    }
-}
-
-// ---- rows behind the last token (warp 10) --------------------------------------------
-
-template <int D>
-__device__ __forceinline__ void cm_zero_tails(const ChunkMmaP &P, CmSmem<D> &sm, const Ctl &c, int lane)
-{
-    RingAt<CmSmem<D>::NST> at;
-    uint32_t phases = 0;  // of each stage's tail barrier
-    for (ChunkWalk<CM_M, CM_NK> it(P.c, sm.share); it.item(); it.next()) {
-        const int n = it.j1 - it.j0;
-        if (n <= 0)
-            continue;
-        if (cm_tail(it)) {
-            auto last = at;
-            last.skip(2 * n - 1);
-            // the next such tile may be many items away, so this warp is more patient than those it serves
-            if (!mbar_await(&sm.tail[last.i], (phases >> last.i) & 1, Ctl{c.status, 64 * c.wait_ns}))
-                return;
-            phases ^= 1u << last.i;
-            const int from = it.r.kv - (it.all - 1) * CM_NK, to = (from + 15) & ~15;
-            for (int i = lane; i < (to - from) * 8 * CmSmem<D>::HALVES; i += 32) {
-                const int half = i / ((to - from) * 8), rest = i - half * (to - from) * 8;
-                *reinterpret_cast<uint4 *>(sm.ring[last.i] + half * (CM_NK * 128) + (from + rest / 8) * 128 +
-                                           (rest % 8) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sm.full[last.i]);
-        }
-        at.skip(2 * n);
     }
 }
 
@@ -277,9 +236,21 @@ __device__ __forceinline__ bool cm_issue(const ChunkMmaP &P, CmSmem<D> &sm, cons
         __syncwarp();
         at.next();
     };
-    // O (+)= P V with the stage's V over `steps` groups of 16 keys, the first four as soon as their weights are
-    // there; the stage is then free
-    const auto product = [&](int stage, int steps, bool first, bool last) {
+    // O (+)= P V with the stage's V, `keys` of whose keys (or all) count, in groups of 16, the first four as soon as
+    // their weights are there; the stage is then free
+    const auto product = [&](int stage, int keys, bool first, bool last, bool tail) {
+        const int steps = (min(CM_NK, keys) + 15) / 16;
+        if (tail) {
+            // (both warps write the same zeros: neither waits for the other)
+            const int gap = steps * 16 - keys;
+            for (int i = threadIdx.x & 31; i < gap * 8 * SM::HALVES; i += 32) {
+                const int half = i / (gap * 8), rest = i - half * gap * 8;
+                *reinterpret_cast<uint4 *>(sm.ring[stage] + half * (CM_NK * 128) + (keys + rest / 8) * 128 +
+                                           (rest % 8) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+        }
         const uint32_t v = ring + stage * (SM::TILE >> 4) + ((CM_NK * 128 >> 4) << 16);
         const auto some = [&](int from, int to_step) {
             for (int s = from; s < to_step; ++s)
@@ -329,7 +300,8 @@ __device__ __forceinline__ bool cm_issue(const ChunkMmaP &P, CmSmem<D> &sm, cons
         if (n <= 0)
             continue;
         const bool one = it.rows <= 128;
-        const auto steps = [&](int j) { return (min(CM_NK, it.limit - (it.j0 + j) * CM_NK) + 15) / 16; };
+        const auto keys = [&](int j) { return it.limit - (it.j0 + j) * CM_NK; };  // from tile j on
+        const bool tail = cm_tail(it);
         if (!mbar_await(&sm.q_full, items & 1, c))
             return false;
         ++items;
@@ -355,7 +327,7 @@ __device__ __forceinline__ bool cm_issue(const ChunkMmaP &P, CmSmem<D> &sm, cons
                         return false;
                     continue;
                 }
-                if (!landed() || !product(at.i, steps(j), j < 2, j + 2 >= n))
+                if (!landed() || !product(at.i, keys(j), j < 2, j + 2 >= n, tail && j + 1 == n))
                     return false;
                 at.next();
                 if (j + 2 < n) {
@@ -383,7 +355,7 @@ __device__ __forceinline__ bool cm_issue(const ChunkMmaP &P, CmSmem<D> &sm, cons
             at.next();
             if (j + 1 < n && !landed())
                 return false;
-            if (!product(vs, steps(j), j == 0, j + 1 == n))
+            if (!product(vs, keys(j), j == 0, j + 1 == n, tail && j + 1 == n))
                 return false;
             if (j + 1 < n) {
                 scores(q);
@@ -678,11 +650,10 @@ __global__ void __launch_bounds__(CM_NT, 1) k_chunk_mma(const __grid_constant__ 
     allow_dependents();  // only the merge follows, which waits for this kernel's end
     if (tid == 0) {
         for (int i = 0; i < CmSmem<D>::NST; ++i) {
-            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.full[i], 2);
             mbar_init(&sm.empty[i], 2);
-            mbar_init(&sm.tail[i], 1);
         }
-        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.q_full, 2);
         mbar_init(&sm.q_empty, 2);
         for (int g = 0; g < 2; ++g) {
             mbar_init(&sm.s_full[g], 1);
@@ -716,10 +687,8 @@ __global__ void __launch_bounds__(CM_NT, 1) k_chunk_mma(const __grid_constant__ 
         cm_softmax<D>(P, sm, c);
     } else {
         regs_give<88>();
-        if (warp == 8) {
-            cm_load<D>(P, sm, c, lane);
-        } else if (warp == 10) {
-            cm_zero_tails<D>(P, sm, c, lane);
+        if (warp == 8 || warp == 10) {
+            cm_load<D>(P, sm, c, lane, warp == 10);
         } else if (const int g = warp == 11; !cm_issue<D>(P, sm, c, g)) {
             if (elect_one())
                 mma_commit(&sm.drained[g]);
