@@ -114,45 +114,19 @@ __device__ __forceinline__ void cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const
         const int n = it.j1 - it.j0;
         if (n <= 0)
             continue;
-        const bool one = it.rows <= 128;
-        // this lane's page of tile j (lanes below `per`)
+        const int ahead = it.rows <= 128 ? 2 : 1;  // key tiles whose scores are formed ahead of a tile's product
+        // this lane's table entry of tile j (lanes below `per`), looked at only when the tile is issued
         const auto page = [&](int j) {
-            if (lane >= per)
+            const int key = (it.j0 + j) * CM_NK + lane * rows;
+            if (lane >= per || j >= n || key >= it.limit)
                 return -1;
-            const int key = j * CM_NK + lane * rows;
-            if (key >= it.limit)
-                return -1;
-            const int p = page_of(G, it.b, key);
-            bad = bad || (p < 0 && w == 0);
-            return p;
+            return __ldg(G.table + it.b * G.table_stride + (key >> G.page_log2));
         };
-        const auto load = [&](const CUtensorMap *map, int j, int p) {
-            if (!mbar_await(&sm.empty[at.i], at.phase ^ 1, c))
-                return false;
-            uint64_t *bar = &sm.full[at.i];
-            const int boxes = min(per, (it.limit - j * CM_NK + rows - 1) / rows);
-            const bool lead = elect_one();
-            // box i of columns 64 h is this warp's when i HALVES + h is of its parity
-            if (lead)
-                mbar_arrive_expect_tx(bar, (D == 128 ? boxes : (boxes + 1 - w) / 2) * box);
-            const int row = j * CM_NK & ((1 << G.page_log2) - 1);  // a tile begins a page, or its second half
-            unsigned char *dst = sm.ring[at.i] + (D == 128 ? w * (CM_NK * 128) : 0);
-            // (one lane issues all its boxes: lanes that issue one each are served one after another, and slower)
-            for (int i = D == 128 ? 0 : w; i < boxes; i += D == 128 ? 1 : 2) {
-                const int page = __shfl_sync(0xffffffffu, p < 0 ? P.none : p, i);
-                if (lead)
-                    tma_load4(dst + i * rows * 128, map, D == 128 ? 64 * w : 0, row, it.h, page, bar);
-            }
-            __syncwarp();
-            at.next();
-            ++issued;
-            return true;
-        };
-        int p0 = page(it.j0), p1 = n > 1 ? page(it.j0 + 1) : -1;
+        int next_k = page(0);
         if (!mbar_await(&sm.q_empty, (items & 1) ^ 1, c))
             break;
         if (elect_one()) {
-            const int tiles = one ? 1 : 2, toks = 128 >> A.g_log2;
+            const int tiles = it.rows <= 128 ? 1 : 2, toks = 128 >> A.g_log2;
             mbar_arrive_expect_tx(&sm.q_full, D == 128 || w == 0 ? tiles * (128 * 128) : 0);
             if (D == 128 || w == 0)
                 for (int t = 0; t < tiles; ++t)
@@ -160,17 +134,42 @@ __device__ __forceinline__ void cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const
         }
         __syncwarp();
         ++items;
-        const int ahead = one ? 2 : 1;  // key tiles whose scores are formed ahead of a tile's product with V
-        bool ok = load(&P.k, it.j0, p0);
-        if (one && n > 1)
-            ok = ok && load(&P.k, it.j0 + 1, p1);
-        for (int j = 0; j < n && ok; ++j) {
-            const int p2 = one && j + 2 < n ? page(it.j0 + j + 2) : -1;
-            ok = load(&P.v, it.j0 + j, p0);
-            if (j + ahead < n)
-                ok = ok && load(&P.k, it.j0 + j + ahead, one ? p2 : p1);
-            p0 = p1;
-            p1 = one ? p2 : (j + 2 < n ? page(it.j0 + j + 2) : -1);
+        // the ring's order: K0 V0 K1 V1 ..., or with one row tile K0 K1 V0 K2 V1 ...
+        bool ok = true;
+        int kj = 0, page0 = -1, page1 = -1;  // the pages of tiles vj and vj + 1
+        for (int vj = 0; vj < n && ok;) {
+            const bool is_k = kj < min(n, vj + ahead);
+            const int j = is_k ? kj : vj, entry = is_k ? next_k : page0;
+            if (is_k) {
+                (kj == vj ? page0 : page1) = next_k;
+                next_k = page(++kj);
+            } else {
+                page0 = page1;
+                ++vj;
+            }
+            if (!mbar_await(&sm.empty[at.i], at.phase ^ 1, c)) {
+                ok = false;
+                break;
+            }
+            uint64_t *bar = &sm.full[at.i];
+            const int boxes = min(per, (it.limit - (it.j0 + j) * CM_NK + rows - 1) / rows);
+            const bool lead = elect_one(), there = entry >= 0 && entry < G.pages;
+            bad = bad || (w == 0 && lane < boxes && !there);
+            // box i of columns 64 h is this warp's when i HALVES + h is of its parity
+            if (lead)
+                mbar_arrive_expect_tx(bar, (D == 128 ? boxes : (boxes + 1 - w) / 2) * box);
+            const int row = (it.j0 + j) * CM_NK & ((1 << G.page_log2) - 1);  // a tile begins a page, or its second half
+            unsigned char *dst = sm.ring[at.i] + (D == 128 ? w * (CM_NK * 128) : 0);
+            const CUtensorMap *map = is_k ? &P.k : &P.v;
+            // (one lane issues all its boxes: lanes that issue one each are served one after another, and slower)
+            for (int i = D == 128 ? 0 : w; i < boxes; i += D == 128 ? 1 : 2) {
+                const int pg = __shfl_sync(0xffffffffu, there ? entry : P.none, i);
+                if (lead)
+                    tma_load4(dst + i * rows * 128, map, D == 128 ? 64 * w : 0, row, it.h, pg, bar);
+            }
+            __syncwarp();
+            at.next();
+            ++issued;
         }
         if (!ok)
             break;
