@@ -17,7 +17,6 @@ namespace hkv {
 // 16 x 16 threads; thread (y, x) holds rows y + 16 i and, of a tile's 64 keys,
 // x + 16 j; of the output columns 4 x + 64 c. K and V tiles land by cp.async;
 // the weights take K's place in shared memory once the scores are formed.
-// M = 64 rows an item for prompts, 16 where single tokens make up the batch.
 // =============================================================================
 
 constexpr int FC_NT = 256;
@@ -217,6 +216,194 @@ __global__ void __launch_bounds__(FC_NT, 2) k_chunk_fma(const __grid_constant__ 
 }
 
 // =============================================================================
+// 32-bit kernel for single tokens
+//
+// An item is one token's G rows of a KV head. Each warp takes key groups of
+// its own (every FR_WARPS-th of 32 keys) and keeps a maximum, sum and output
+// for each row; the warps meet at the item's end. Scores: four keys at a time,
+// 8 lanes a key, each lane D/8 elements against its part of the G queries in
+// registers (two and 16 at G = 8). Output: a lane holds D/32 columns, V rows are read whole by the
+// warp. K and V go from memory to registers and are used once for all G rows:
+// HBM-bound, 8 x G FMAs a lane for 16 bytes each.
+// =============================================================================
+
+constexpr int FR_WARPS = 8;
+constexpr int FR_NK = 256;  // keys of a tile: one group a warp
+
+template <int D, int G>
+struct FrSmem {
+    ChunkShare share;
+    unsigned long long red[FR_WARPS];
+    float m[FR_WARPS][G], l[FR_WARPS][G], o[FR_WARPS][G][D];
+};
+
+template <int D, int G>
+__global__ void __launch_bounds__(FR_WARPS * 32, 2) k_chunk_rows(const __grid_constant__ ChunkP P)
+{
+    constexpr int LK = G == 8 ? 16 : 8;    // lanes of a key (the queries' part fits in registers)
+    constexpr int KS = 32 / LK;            // keys at a time
+    constexpr int E = D / LK, C = D / 32;  // elements of a key a lane, output columns a lane
+    __shared__ FrSmem<D, G> sm;
+    wait_prior_grid();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LK, kq = lane / LK;
+    if (threadIdx.x == 0)
+        P.desc[blockIdx.x].n = 0;
+    chunk_share<FR_WARPS * 32, G, FR_NK>(P, sm.red, &sm.share);
+    const int64_t rec = (int64_t)P.rec_rows * (D + 2);
+    bool bad = false;
+    for (ChunkWalk<G, FR_NK> it(P, sm.share); it.item(); it.next()) {
+        if (!it.mine())
+            continue;
+        float q[G][E];
+        const char *qrow = P.q + it.row0 * P.qs + (int64_t)it.h * G * D * 4;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int i = 0; i < E; i += 4) {
+                const float4 x = __ldg(reinterpret_cast<const float4 *>(qrow + (g * D + LK * i + 4 * sub) * 4));
+                q[g][i] = x.x, q[g][i + 1] = x.y, q[g][i + 2] = x.z, q[g][i + 3] = x.w;
+            }
+        float m[G], l[G], o[G][C];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            m[g] = -INFINITY;
+            l[g] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                o[g][c] = 0.0f;
+        }
+        for (int j = it.j0; j < it.j1; ++j) {
+            const int key0 = j * FR_NK + warp * 32, n = min(32, it.limit - key0);
+            if (n <= 0)
+                continue;
+            // lane i: key key0 + i's row, or -1
+            int64_t at = -1;
+            if (lane < n) {
+                const int p = page_of(P.pages, it.b, key0 + lane);
+                bad = bad || p < 0;
+                if (p >= 0)
+                    at = row_offset(P.pages, p, it.h, key0 + lane);
+            }
+            float s[G];  // lane i: the scores of key key0 + i
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                s[g] = -INFINITY;
+#pragma unroll 2
+            for (int k = 0; k < 32; k += KS) {
+                if (k >= n)
+                    break;
+                const int64_t row = __shfl_sync(0xffffffffu, at, k + kq);
+                float x[E];
+#pragma unroll
+                for (int i = 0; i < E; i += 4) {
+                    const float4 v = row < 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                             : __ldg(reinterpret_cast<const float4 *>(P.pages.k + row + (LK * i + 4 * sub) * 4));
+                    x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+                }
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    float d = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < E; ++i)
+                        d = fmaf(q[g][i], x[i], d);
+#pragma unroll
+                    for (int i = 1; i < LK; i *= 2)
+                        d += __shfl_xor_sync(0xffffffffu, d, i);
+                    // key k + i is with the lanes LK i ..
+                    const float mine = __shfl_sync(0xffffffffu, d, LK * (lane % KS));
+                    if (lane / KS == k / KS)
+                        s[g] = mine;
+                }
+            }
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                s[g] = at < 0 ? -INFINITY : s[g] * P.scale_log2;
+                const float mn = fmaxf(m[g], warp_max(s[g]));
+                const float ref = mn == -INFINITY ? 0.0f : mn;  // nothing yet: all weights 0
+                const float f = ex2(m[g] - ref);
+                s[g] = ex2(s[g] - ref);
+                m[g] = mn;
+                l[g] = l[g] * f + s[g];  // this lane's keys; summed over the lanes at the end
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    o[g][c] *= f;
+            }
+#pragma unroll 8
+            for (int k = 0; k < n; ++k) {
+                const int64_t row = __shfl_sync(0xffffffffu, at, k);
+                float v[C];
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    v[c] = 0.0f;
+                if (row >= 0) {
+                    const char *src = P.pages.v + row + lane * C * 4;
+                    if constexpr (C == 4) {
+                        const float4 x = __ldg(reinterpret_cast<const float4 *>(src));
+                        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+                    } else {
+                        const float2 x = __ldg(reinterpret_cast<const float2 *>(src));
+                        v[0] = x.x, v[1] = x.y;
+                    }
+                }
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const float p = __shfl_sync(0xffffffffu, s[g], k);
+#pragma unroll
+                    for (int c = 0; c < C; ++c)
+                        o[g][c] = fmaf(p, v[c], o[g][c]);
+                }
+            }
+        }
+        // the warps' parts together, in warp order
+        __syncthreads();  // the item before has been read
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const float sum = warp_sum(l[g]);
+            if (lane == 0) {
+                sm.m[warp][g] = m[g];
+                sm.l[warp][g] = sum;
+            }
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                sm.o[warp][g][lane * C + c] = o[g][c];
+        }
+        __syncthreads();
+        const bool whole = it.whole();
+        float *record = P.part + (2 * (int64_t)blockIdx.x + (it.first_part() ? 1 : 0)) * rec;
+        for (int i = threadIdx.x; i < G * D; i += FR_WARPS * 32) {
+            const int g = i / D, d = i - g * D;
+            float M = -INFINITY, L = 0.0f, x = 0.0f;
+#pragma unroll
+            for (int w = 0; w < FR_WARPS; ++w)
+                M = fmaxf(M, sm.m[w][g]);
+            const float ref = M == -INFINITY ? 0.0f : M;
+#pragma unroll
+            for (int w = 0; w < FR_WARPS; ++w) {
+                const float f = ex2(sm.m[w][g] - ref);
+                L = fmaf(sm.l[w][g], f, L);
+                x = fmaf(sm.o[w][g][d], f, x);
+            }
+            const int64_t at = (int64_t)it.row0 * P.Hq + it.h * G + g;
+            if (whole) {
+                reinterpret_cast<float *>(P.out)[at * D + d] = L > 0.0f ? x / L : 0.0f;
+                if (d == 0 && P.lse != nullptr)
+                    P.lse[at] = L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+            } else {
+                record[(int64_t)g * D + d] = x;
+                if (d == 0) {
+                    record[(int64_t)P.rec_rows * D + g] = M;
+                    record[(int64_t)P.rec_rows * (D + 1) + g] = L;
+                }
+            }
+        }
+        if (threadIdx.x == 0 && !whole && it.first_part())
+            P.desc[blockIdx.x] = ChunkDesc{it.parts(), it.row0, it.h, it.rows};
+    }
+    if (bad)
+        atomicOr(P.status, HKV_DEV_BAD_INDEX);
+}
+
+// =============================================================================
 // Host side
 // =============================================================================
 
@@ -297,10 +484,17 @@ static hkv_status run_mma(const hkv_problem *p, const ChunkP &A, int ctas, cudaS
 template <int D>
 static hkv_status run_fma(const ChunkP &P, int ctas, cudaStream_t st)
 {
-    // single tokens: items of 16 rows, fewer wasted
-    const bool few = ((int64_t)P.T << P.g_log2) <= 16 * (int64_t)P.B;
-    hkv_status s = few ? launch_dependent(k_chunk_fma<D, 16>, ctas, FC_NT, sizeof(FcSmem<D, 16>), st, P)
-                       : launch_dependent(k_chunk_fma<D, FC_M>, ctas, FC_NT, sizeof(FcSmem<D, FC_M>), st, P);
+    hkv_status s;
+    // No more rows than requests: single tokens, as far as the host can tell (any lengths are right in either kernel)
+    if (P.T <= P.B) {
+        const auto rows = P.g_log2 == 0   ? k_chunk_rows<D, 1>
+                          : P.g_log2 == 1 ? k_chunk_rows<D, 2>
+                          : P.g_log2 == 2 ? k_chunk_rows<D, 4>
+                                          : k_chunk_rows<D, 8>;
+        s = launch_dependent(rows, ctas, FR_WARPS * 32, 0, st, P);
+    } else {
+        s = launch_dependent(k_chunk_fma<D, FC_M>, ctas, FC_NT, sizeof(FcSmem<D, FC_M>), st, P);
+    }
     if (s != HKV_OK)
         return s;
     return launch_dependent(k_chunk_merge<4, D>, merge_blocks(P, ctas), CMERGE_NT, 0, st, P);
