@@ -22,34 +22,35 @@ namespace hkv {
 constexpr int FC_NT = 256;
 constexpr int FC_NK = 64;
 constexpr int FC_M = 64;
+using FcLine = ChunkLine<FC_M, FC_NK, 1, 1>;
 
-template <int D, int M>
+template <int D>
 struct FcSmem {
-    float q[M][D + 4];
-    float k[FC_NK][D + 4];  // then the weights, [M][FC_NK + 4]
+    float q[FC_M][D + 4];
+    float k[FC_NK][D + 4];  // then the weights, [FC_M][FC_NK + 4]
     float v[FC_NK][D];
     ChunkShare share;
     unsigned long long red[FC_NT / 32];
     int ok[FC_NK];  // the tile's keys that are there
 };
 
-template <int D, int M>
+template <int D>
 __global__ void __launch_bounds__(FC_NT, 2) k_chunk_fma(const __grid_constant__ ChunkP P)
 {
     extern __shared__ __align__(128) unsigned char smem_raw[];
-    auto &sm = *reinterpret_cast<FcSmem<D, M> *>(smem_raw);
-    constexpr int RT = M / 16, CT = D / 64;
+    auto &sm = *reinterpret_cast<FcSmem<D> *>(smem_raw);
+    constexpr int M = FC_M, RT = M / 16, CT = D / 64;
     static_assert(M * (FC_NK + 4) <= FC_NK * (D + 4), "the weights fit in K's place");
     float(*w)[FC_NK + 4] = reinterpret_cast<float(*)[FC_NK + 4]>(&sm.k[0][0]);
     wait_prior_grid();
     const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
     if (tid == 0)
         P.desc[blockIdx.x].n = 0;
-    chunk_share<FC_NT, M, FC_NK>(P, sm.red, &sm.share);
+    chunk_share<FC_NT, FcLine>(P, sm.red, &sm.share);
     const int G = 1 << P.g_log2;
     const int64_t rec = (int64_t)P.rec_rows * (D + 2);
     bool bad = false;
-    for (ChunkWalk<M, FC_NK> it(P, sm.share); it.item(); it.next()) {
+    for (ChunkWalk<FcLine> it(P, sm.share); it.item(); it.next()) {
         if (!it.mine())
             continue;
         __syncthreads();  // the item before is done with q
@@ -227,8 +228,8 @@ __global__ void __launch_bounds__(FC_NT, 2) k_chunk_fma(const __grid_constant__ 
 // HBM-bound, 8 x G FMAs a lane for 16 bytes each.
 // =============================================================================
 
-constexpr int FR_WARPS = 8;
-constexpr int FR_NK = 256;  // keys of a tile: one group a warp
+constexpr int FR_WARPS = 4;
+constexpr int FR_NK = 32 * FR_WARPS;  // keys of a tile: one group a warp
 
 template <int D, int G>
 struct FrSmem {
@@ -238,9 +239,10 @@ struct FrSmem {
 };
 
 template <int D, int G>
-__global__ void __launch_bounds__(FR_WARPS * 32, 2) k_chunk_rows(const __grid_constant__ ChunkP P)
+__global__ void __launch_bounds__(FR_WARPS * 32, 4) k_chunk_rows(const __grid_constant__ ChunkP P)
 {
     constexpr int LK = G == 8 ? 16 : 8;    // lanes of a key (the queries' part fits in registers)
+    using Line = ChunkLine<G, FR_NK, 1, 1>;
     constexpr int KS = 32 / LK;            // keys at a time
     constexpr int E = D / LK, C = D / 32;  // elements of a key a lane, output columns a lane
     __shared__ FrSmem<D, G> sm;
@@ -248,10 +250,10 @@ __global__ void __launch_bounds__(FR_WARPS * 32, 2) k_chunk_rows(const __grid_co
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LK, kq = lane / LK;
     if (threadIdx.x == 0)
         P.desc[blockIdx.x].n = 0;
-    chunk_share<FR_WARPS * 32, G, FR_NK>(P, sm.red, &sm.share);
+    chunk_share<FR_WARPS * 32, Line>(P, sm.red, &sm.share);
     const int64_t rec = (int64_t)P.rec_rows * (D + 2);
     bool bad = false;
-    for (ChunkWalk<G, FR_NK> it(P, sm.share); it.item(); it.next()) {
+    for (ChunkWalk<Line> it(P, sm.share); it.item(); it.next()) {
         if (!it.mine())
             continue;
         float q[G][E];
@@ -417,7 +419,7 @@ static ChunkWs chunk_ws(const hkv_problem *p, int32_t tokens)
     ChunkWs w{};
     const int sms = sm_count() > 0 ? sm_count() : 148;
     const bool bf = p->dtype == HKV_BF16;
-    w.ctas = bf ? sms : 2 * sms;
+    w.ctas = bf ? sms : 4 * sms;  // fp32: single tokens in CTAs of half the threads
     const int64_t rows = std::min<int64_t>(bf ? CM_M : FC_M, (int64_t)tokens * (p->Hq / p->Hkv));
     w.rec_rows = (int)((rows + 7) / 8 * 8);
     const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -493,7 +495,8 @@ static hkv_status run_fma(const ChunkP &P, int ctas, cudaStream_t st)
                                           : k_chunk_rows<D, 8>;
         s = launch_dependent(rows, ctas, FR_WARPS * 32, 0, st, P);
     } else {
-        s = launch_dependent(k_chunk_fma<D, FC_M>, ctas, FC_NT, sizeof(FcSmem<D, FC_M>), st, P);
+        ctas /= 2;
+        s = launch_dependent(k_chunk_fma<D>, ctas, FC_NT, sizeof(FcSmem<D>), st, P);
     }
     if (s != HKV_OK)
         return s;

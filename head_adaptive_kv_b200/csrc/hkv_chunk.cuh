@@ -4,11 +4,11 @@
 // Item: M rows (M/G tokens of one request, the G query heads of one KV head
 // side by side, so that a K or V row read once serves the whole group). An
 // item's keys come in tiles of NK. All items, request by request, head by
-// head, stand on one line, ITEM_COST + (its tiles) positions each, C in all,
+// head, stand on one line, COST + (its tiles) positions each, C in all,
 // and CTA c of N takes the positions [c C / N, (c+1) C / N): equal work for
 // every CTA whatever the requests' lengths, one token or many. N is the grid,
-// or fewer where that would leave a CTA less than MIN_SHARE positions; the
-// rest of the grid has nothing to do. An item that crosses
+// or fewer where that would leave a CTA less than LEAST positions; the rest of
+// the grid has nothing to do. An item that crosses
 // from one CTA into the next leaves a record (unnormalised output, row
 // maxima and sums) in each, which k_chunk_merge joins in line order; an item
 // within one CTA is written at once. A CTA has at most two records: of the
@@ -19,9 +19,6 @@
 #include "hkv_pages.cuh"
 
 namespace hkv {
-
-constexpr int ITEM_COST = 1;  // line positions of an item beside its tiles
-constexpr int MIN_SHARE = 2;  // positions that a CTA is worth (at least 1: an owner of no position has no record)
 
 struct ChunkDesc {  // the item that starts in a CTA and ends in a later one (n > 1 records), or n = 0
     int32_t n, row0, head, rows;  // row0: first token row; rows: valid rows
@@ -62,10 +59,13 @@ __device__ __forceinline__ ChunkReq chunk_request(const ChunkP &P, int b)
 
 __host__ __device__ constexpr int log2_of(int x) { return x <= 1 ? 0 : 1 + log2_of(x / 2); }
 
-// (All sizes here are powers of two: shifts, as this stands before every
-// call's first load.)
-template <int M, int NK>
+// A kernel's line: M rows an item, NK keys a tile, COST positions of an item
+// beside its tiles (its beginning and end, in tiles), LEAST positions that a
+// CTA is worth (at least 1: an owner of no position has no record). All sizes
+// here are powers of two: shifts, as this stands before every call's first load.
+template <int M_, int NK_, int COST_, int LEAST_>
 struct ChunkLine {
+    static constexpr int M = M_, NK = NK_, COST = COST_, LEAST = LEAST_;
     static constexpr int NKL = log2_of(NK);
     int ttl;  // log2 of an item's tokens
 
@@ -99,13 +99,13 @@ struct ChunkLine {
             };
             s = F(a1 + m) - F(a1);
         }
-        return s + (int64_t)ITEM_COST * m;
+        return s + (int64_t)COST * m;
     }
 
     __device__ __forceinline__ int64_t head_cost(const ChunkReq &r) const
     {
         const int m = items(r);
-        return m == 0 ? 0 : before(r, m - 1) + ITEM_COST + tiles(r, m - 1);
+        return m == 0 ? 0 : before(r, m - 1) + COST + tiles(r, m - 1);
     }
 };
 
@@ -128,10 +128,10 @@ struct ChunkShare {
 };
 
 // Every thread of the CTA (NT of them) calls this. `red`: NT/32 words.
-template <int NT, int M, int NK>
+template <int NT, class Line>
 __device__ __forceinline__ void chunk_share(const ChunkP &P, unsigned long long *red, ChunkShare *sh)
 {
-    const ChunkLine<M, NK> line(P);
+    const Line line(P);
     // the cost of request b0 + this thread, the cost of those before it in the strip, and the strip's
     const auto strip = [&](int b0, ChunkReq &r, int64_t &cost, unsigned long long &sum) {
         const int b = b0 + threadIdx.x;
@@ -157,7 +157,7 @@ __device__ __forceinline__ void chunk_share(const ChunkP &P, unsigned long long 
     }
     if (clamped && blockIdx.x == 0)
         atomicOr(P.status, HKV_DEV_LEN_CLAMPED);
-    const int64_t N = max((int64_t)1, min((int64_t)gridDim.x, line_div(total, MIN_SHARE)));
+    const int64_t N = max((int64_t)1, min((int64_t)gridDim.x, line_div(total, Line::LEAST)));
     const int64_t each = line_div(total, N), more = total - each * N, c = blockIdx.x;
     const int64_t x0 = c >= N ? total : c * each + min(c, more), x1 = c >= N ? total : x0 + each + (c < more ? 1 : 0);
     if (threadIdx.x == 0)
@@ -203,10 +203,10 @@ __device__ __forceinline__ int chunk_owner(const ChunkShare &sh, int64_t x)
 }
 
 // Walks the items of a CTA's share.
-template <int M, int NK>
+template <class Line>
 struct ChunkWalk {
     const ChunkP &P;
-    const ChunkLine<M, NK> line;
+    const Line line;
     const ChunkShare &sh;  // in shared memory
     ChunkReq r;
     int b, h, t, m;
@@ -235,8 +235,8 @@ struct ChunkWalk {
         row0 = r.q0 + tok;
         pos0 = r.kv - r.n + tok;
         limit = max(0, pos0 + toks);
-        all = min(on_line, (limit + NK - 1) / NK);
-        const int64_t p = s + ITEM_COST;
+        all = min(on_line, (limit + Line::NK - 1) / Line::NK);
+        const int64_t p = s + Line::COST;
         j0 = (int)max((int64_t)0, min((int64_t)all, sh.x0 - p));
         j1 = (int)max((int64_t)0, min((int64_t)all, sh.x1 - p));
         end = p + on_line;
@@ -249,7 +249,7 @@ struct ChunkWalk {
     __device__ __forceinline__ bool first_part() const { return j0 == 0; }
     __device__ __forceinline__ int parts() const
     {
-        const int64_t p = s + ITEM_COST;
+        const int64_t p = s + Line::COST;
         return chunk_owner(sh, p + all - 1) - chunk_owner(sh, p) + 1;
     }
 

@@ -39,6 +39,8 @@ namespace hkv {
 
 constexpr int CM_NT = 384;
 constexpr int CM_M = 256, CM_NK = 128;
+// (an item's start and end cost about two tiles: 2048 tokens alone 59 us, 62 counted as one, 59 as three)
+using CmLine = ChunkLine<CM_M, CM_NK, 2, 2>;
 constexpr float CM_GROW = 8.0f;  // log2 of the growth of a score that moves the reference
 
 struct alignas(64) ChunkMmaP {
@@ -85,7 +87,7 @@ struct RingAt {
 // The item's last V tile holds rows behind the request's last token that take
 // part in the product (it runs over whole groups of 16 keys): their weights
 // are 0, but what lies there may be NaN.
-__device__ __forceinline__ bool cm_tail(const ChunkWalk<CM_M, CM_NK> &it)
+__device__ __forceinline__ bool cm_tail(const ChunkWalk<CmLine> &it)
 {
     return it.j1 == it.all && it.limit == it.r.kv && (it.r.kv & 15) != 0;
 }
@@ -110,7 +112,7 @@ __device__ __forceinline__ void cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const
     bool bad = false;
     if (A.withhold)
         return;
-    for (ChunkWalk<CM_M, CM_NK> it(A, sm.share); it.item(); it.next()) {
+    for (ChunkWalk<CmLine> it(A, sm.share); it.item(); it.next()) {
         const int n = it.j1 - it.j0;
         if (n <= 0)
             continue;
@@ -294,7 +296,7 @@ __device__ __forceinline__ bool cm_issue(const ChunkMmaP &P, CmSmem<D> &sm, cons
             mma_commit(&sm.q_empty);
         __syncwarp();
     };
-    for (ChunkWalk<CM_M, CM_NK> it(P.c, sm.share); it.item(); it.next()) {
+    for (ChunkWalk<CmLine> it(P.c, sm.share); it.item(); it.next()) {
         const int n = it.j1 - it.j0;
         if (n <= 0)
             continue;
@@ -379,7 +381,7 @@ __device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, co
     const int G = 1 << A.g_log2;
     const int64_t rec = (int64_t)A.rec_rows * (D + 2);
     uint32_t s_count = 0, o_count = 0, x_count = 0, o_other = 0, turns = 0;  // phases; o_other: of group 1, seen from 0
-    for (ChunkWalk<CM_M, CM_NK> it(A, sm.share); it.item(); it.next()) {
+    for (ChunkWalk<CmLine> it(A, sm.share); it.item(); it.next()) {
         if (!it.mine())
             continue;
         const int n = it.j1 - it.j0;
@@ -677,7 +679,7 @@ __global__ void __launch_bounds__(CM_NT, 1) k_chunk_mma(const __grid_constant__ 
     if (tid == 0)
         P.c.desc[blockIdx.x].n = 0;
     tc_fence_before();
-    chunk_share<CM_NT, CM_M, CM_NK>(P.c, sm.red, &sm.share);  // (its barriers publish the set-up above)
+    chunk_share<CM_NT, CmLine>(P.c, sm.red, &sm.share);  // (its barriers publish the set-up above)
     __syncthreads();
     tc_fence_after();
     // the launch's 384 x 168 registers, as 256 x 208 + 128 x 88: a softmax thread holds a row of S
