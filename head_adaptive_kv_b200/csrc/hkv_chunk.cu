@@ -453,7 +453,7 @@ static hkv_status encode_maps(const hkv_problem *p, const ChunkP &A, ChunkMmaP *
     const cuuint64_t D = (cuuint64_t)p->D;
     const cuuint32_t G = (cuuint32_t)(p->Hq / p->Hkv);
     const cuuint64_t qd[3] = {D, (cuuint64_t)p->Hq, (cuuint64_t)A.T}, qst[2] = {D * 2, (cuuint64_t)A.qs};
-    const cuuint32_t qb[3] = {64, G, 128 / G};
+    const cuuint32_t qb[3] = {64, G, 128 / G}, qb1[3] = {64, G, 1};
     const PagesP &g = A.pages;
     const cuuint64_t page = 1ull << g.page_log2, pages = (cuuint64_t)std::max(g.pages, 1);
     const cuuint64_t kd[4] = {D, page, (cuuint64_t)p->Hkv, pages};
@@ -464,7 +464,7 @@ static hkv_status encode_maps(const hkv_problem *p, const ChunkP &A, ChunkMmaP *
     // an empty pool has no address: no load reads through its maps
     const void *k = g.pages > 0 ? (const void *)g.k : (const void *)A.q, *v = g.pages > 0 ? (const void *)g.v : (const void *)A.q;
     M->none = (int32_t)pages;
-    return encode_box(&M->q, A.q, 3, qd, qst, qb) && encode_box(&M->k, k, 4, kd, kst, kb) &&
+    return encode_box(&M->q, A.q, 3, qd, qst, qb) && encode_box(&M->q1, A.q, 3, qd, qst, qb1) && encode_box(&M->k, k, 4, kd, kst, kb) &&
                    encode_box(&M->v, v, 4, kd, kst, kb)
                ? HKV_OK
                : HKV_ERR_INVALID_ARG;

@@ -45,7 +45,7 @@ constexpr float CM_GROW = 8.0f;  // log2 of the growth of a score that moves the
 
 struct alignas(64) ChunkMmaP {
     ChunkP c;
-    CUtensorMap q, k, v;
+    CUtensorMap q, q1, k, v;  // q1: boxes of one token's group
     int32_t none;  // a page coordinate outside the pool: the load gives zeros
 };
 
@@ -129,10 +129,17 @@ __device__ __forceinline__ void cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const
             break;
         if (elect_one()) {
             const int tiles = it.rows <= 128 ? 1 : 2, toks = 128 >> A.g_log2;
-            mbar_arrive_expect_tx(&sm.q_full, D == 128 || w == 0 ? tiles * (128 * 128) : 0);
-            if (D == 128 || w == 0)
-                for (int t = 0; t < tiles; ++t)
-                    tma_load3(sm.q[t] + w * (128 * 128), &P.q, 64 * w, it.h << A.g_log2, it.row0 + t * toks, &sm.q_full);
+            const bool single = it.rows == 1 << A.g_log2, mine = D == 128 || w == 0;
+            mbar_arrive_expect_tx(&sm.q_full, !mine ? 0 : single ? it.rows * 128 : tiles * (128 * 128));
+            if (mine) {
+                // (a single token leaves the other rows as they were, zero as a rule: products of zeros cost no power)
+                if (single)
+                    tma_load3(sm.q[0] + w * (128 * 128), &P.q1, 64 * w, it.h << A.g_log2, it.row0, &sm.q_full);
+                else
+                    for (int t = 0; t < tiles; ++t)
+                        tma_load3(sm.q[t] + w * (128 * 128), &P.q, 64 * w, it.h << A.g_log2, it.row0 + t * toks,
+                                  &sm.q_full);
+            }
         }
         __syncwarp();
         ++items;
@@ -453,7 +460,8 @@ __device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, co
                         }
                     }
                 }
-                const float ref = m == -INFINITY ? 0.0f : m * sc;
+                // (rows that are not there weigh nothing: zeros again)
+                const float ref = r >= it.rows ? INFINITY : m == -INFINITY ? 0.0f : m * sc;
                 const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(-ref, -ref);
                 float2 sum[2] = {make_float2(l, 0.0f), make_float2(0.0f, 0.0f)};
                 // weights of columns 32 i .. 32 i + 31 as bf16 pairs
@@ -672,8 +680,11 @@ __global__ void __launch_bounds__(CM_NT, 1) k_chunk_mma(const __grid_constant__ 
     }
     if (warp == 9)
         tmem_alloc(&sm.tmem, 512);
-    if (warp == 8 && lane < 3)
-        tma_prefetch_map(lane == 0 ? &P.q : lane == 1 ? &P.k : &P.v);
+    if (warp == 8 && lane < 4)
+        tma_prefetch_map(lane == 0 ? &P.q : lane == 1 ? &P.k : lane == 2 ? &P.v : &P.q1);
+    for (int i = tid; i < (int)sizeof(sm.q[0]) / 16; i += CM_NT)
+        reinterpret_cast<uint4 *>(sm.q[0])[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
     wait_prior_grid();
     const Ctl c{P.c.status, P.c.wait_ns};
     if (tid == 0)
