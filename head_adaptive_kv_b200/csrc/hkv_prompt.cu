@@ -540,7 +540,7 @@ hkv_status check_pages(const hkv_pages *g, const hkv_problem *p, bool storage, b
         (g->page != 16 && g->page != 32 && g->page != 64 && g->page != 128 && g->page != 256) ||
         (int64_t)g->pages * g->page >= (1ll << 31))
         return HKV_ERR_INVALID_ARG;
-    if (table && (g->table_cols < 0 || g->table_stride < g->table_cols || (int64_t)g->table_cols * g->page >= (1ll << 31) ||
+    if (table && (g->table_cols < 0 || g->table_stride < g->table_cols || (int64_t)g->table_cols * g->page > (1ll << 30) ||
                   (g->table_cols > 0 && !words(g->table))))
         return HKV_ERR_INVALID_ARG;
     if (storage) {

@@ -295,7 +295,7 @@ def page_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, state: PageState, af
               ws: StatusWorkspace, granted: Optional[torch.Tensor] = None, stream=None):
     """Block tables, slot map and positions for new_len[b] tokens behind the ctx_len[b] cached ones of each request
     (int32 [B]; see hkv_page_plan). `after` receives the state: it shares `state`'s tables and stack, and may be
-    `state` itself. chunk is written; granted: optional int32 [B], the tokens each request was given (0 where it was
+    `state` itself, as chunk.kv_len may be ctx_len. chunk is written; granted: optional int32 [B], the tokens each request was given (0 where it was
     left out)."""
     B = state._rows
     _int32(ctx_len, B, "ctx_len")
@@ -334,7 +334,7 @@ def _rows(t: torch.Tensor, dtype: torch.dtype, shape: tuple, what: str) -> int:
     s = t.stride()
     if s[2] != 1 or (heads > 1 and s[1] != D):
         raise ValueError(f"{what}: heads and D must be contiguous")
-    return s[0] if tokens > 1 else max(s[0], heads * D)
+    return s[0] if tokens > 1 else heads * D
 
 
 def _contiguous(t: torch.Tensor, dtype: torch.dtype, shape: tuple, what: str):

@@ -40,7 +40,7 @@ extern "C" {
 
 /* The page pool: K and V of page i, KV head h, row t at
  * i*stride_p + h*stride_h + t*stride_t (elements; D contiguous; 16-byte
- * aligned like a tier's rows), and the block tables: column c of row b names
+ * aligned like a tier's rows, strides above 0 where there is more than one), and the block tables: column c of row b names
  * the page of tokens c*page .. c*page + page-1 of request b. Any other entry
  * than a page of the pool means that the tokens are not there: they are masked
  * (attention), read as zeros (fill) or not written, and HKV_DEV_BAD_INDEX is
@@ -52,7 +52,7 @@ typedef struct {
     int32_t page;                          /* tokens a page: 16, 32, 64, 128 or 256 */
     int32_t *table;                        /* device [B, table_cols], row stride table_stride */
     int64_t table_stride;
-    int32_t table_cols;
+    int32_t table_cols;                    /* table_cols*page at most 2^30 */
 } hkv_pages;
 
 /* Allocation state beside the tables, all int32 on the device: `free` is a
@@ -88,7 +88,8 @@ typedef struct {
  * out too, with HKV_DEV_BAD_INDEX. The j-th page given out is free[free_count-1-j],
  * to the requests in order, columns ascending.
  * - in, after: the state before and after. They may be the same; `free` has to be
- *   (this call does not write it). Nothing else may overlap.
+ *   (this call does not write it). out->kv_len may be ctx_len, so that a loop's
+ *   lengths advance in place. Nothing else may overlap.
  * - pages: page, pages and the table (written at the new columns); K and V are
  *   not used and may be NULL.
  * - granted: device int32 [B] or NULL, the new tokens each request was given.
@@ -128,8 +129,8 @@ typedef struct {
  *   left as they are).
  * - K and V rows go to the pages at slot[row] (pages and slot given; -1 = not
  *   written; another slot outside the pool is not written either and sets
- *   HKV_DEV_BAD_INDEX; rows of one call that share a slot leave either row's
- *   values in it), or to k_out, v_out [tokens, Hkv, D] contiguous (given
+ *   HKV_DEV_BAD_INDEX; rows of one call that share a slot leave a mixture of
+ *   their values in it), or to k_out, v_out [tokens, Hkv, D] contiguous (given
  *   instead; the layout of hkv_append's k_new, v_new), which may be k and v.
  * - q_w, k_w: device [D] of the problem's type, both or neither, 16-byte
  *   aligned; eps >= 0.

@@ -59,7 +59,7 @@ class Case:
         got, want = f64(self.lse)[:n], ref[1][:n]
         none = np.isneginf(want)
         assert np.array_equal(np.isneginf(got), none)
-        assert (np.abs(got - want)[~none] <= lse_tol[:n][~none]).all()
+        assert (np.abs(got[~none] - want[~none]) <= lse_tol[:n][~none]).all()
         assert (self.out[n:] == 5.0).all() and (self.lse[n:] == 5.0).all()  # rows behind the last sequence
 
 
@@ -359,4 +359,39 @@ def test_waits_that_run_out_end_the_call():
     assert c.ws.status() == hkv.DEV_TIMEOUT
     c.ws.init()
     c.out.fill_(5.0), c.lse.fill_(5.0)
+    c.run().check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_many_requests(dtype):
+    """More requests than a CTA has threads: single tokens, some requests without any, and a mixed batch."""
+    single = [(7 * i % 300, 0 if i % 11 == 5 else 1) for i in range(900)]
+    Case(single, 2, 2, 64, dtype, 16, seed=18).run().check()
+    mixed = [(5 * i % 40, 1 + i % 3) for i in range(800)]
+    Case(mixed, 2, 1, 64, dtype, 16, seed=19).run().check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_single_tokens_in_a_batch_of_more_rows(dtype):
+    """Rows above the requests' count pick the kernel for chunks; the lengths may be single tokens all the same, and
+    fewer rows than requests may hold one longer chunk."""
+    c = Case([(500, 1), (0, 1), (90, 1)], 8, 2, 128, dtype, 32, pad=200, seed=20)
+    c.run().check()
+    Case([(500, 3), (40, 0), (90, 0), (7, 0)], 8, 2, 128, dtype, 32, seed=21).run().check()
+
+
+def test_an_empty_pool():
+    for dtype in (BF, F32):
+        c = Case([(3, 2), (0, 1)], 4, 2, 64, dtype, 16, seed=22)
+        c.k, c.v = c.k[:0], c.v[:0]
+        c.run()
+        assert c.ws.status() == hkv.DEV_BAD_INDEX
+        assert (c.out == 0).all() and torch.isneginf(c.lse).all()
+
+
+def test_one_row_of_any_stride():
+    c = Case([(40, 1)], 8, 2, 128, BF, 32, seed=23)
+    wide = torch.zeros(1, 8 * 128 + 3, dtype=BF, device=DEV)
+    wide[:, :1024] = c.q.reshape(1, 1024)
+    c.q = wide[:, :1024].unflatten(1, (8, 128))
     c.run().check()

@@ -141,6 +141,23 @@ def test_release_and_plan_over_many_steps():
         assert int(st.free_count) == count
 
 
+def test_plan_advances_lengths_in_place():
+    """ctx_len and kv_len one tensor: each call's lengths are the next one's."""
+    B, page = 700, 16  # more requests than the scan's strip
+    st, ch = prompt.PageState.allocate(B, 4, page, 4 * B, DEV), prompt.Chunk.allocate(B, 3 * B, DEV)
+    ws = prompt.status_workspace(DEV)
+    ctx = np.zeros(B, np.int32)
+    held, free, count, table = ctx.copy(), st.free.cpu().numpy(), 4 * B, st.table.cpu().numpy()
+    for step in range(6):
+        new = (np.arange(B) + step) % 5
+        prompt.page_plan(ch.kv_len, i32(new), st, st, ch, ws)
+        r = op.plan(ctx, new, held, free, count, table, page, 3 * B)
+        ctx, held, count, table = r["kv_len"], r["held"], r["count"], r["table"]
+        assert np.array_equal(ch.kv_len.cpu().numpy(), ctx) and np.array_equal(ch.slot.cpu().numpy(), r["slot"])
+        assert np.array_equal(st.table.cpu().numpy(), table) and int(st.free_count) == count
+    assert ws.status() == 0
+
+
 def test_release_of_a_state_that_does_not_fit():
     st = prompt.PageState.allocate(3, 4, 16, 10, DEV)
     ws = prompt.status_workspace(DEV)

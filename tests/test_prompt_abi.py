@@ -64,7 +64,7 @@ def _pages(pr, **kw):
 BAD_PAGES = {
     "page 24": dict(page=24), "page 8": dict(page=8), "page 512": dict(page=512), "page 0": dict(page=0),
     "negative pool": dict(pages=-1), "slots past 31 bits": dict(pages=1 << 27), "row stride": dict(table_stride=3),
-    "no table": dict(table=None), "table alignment": dict(table=3 * A + 2),
+    "table past 2^30 tokens": dict(table_stride=1 << 27, table_cols=(1 << 26) + 1), "no table": dict(table=None), "table alignment": dict(table=3 * A + 2),
 }
 BAD_STORAGE = {
     "no K": dict(k=None), "no V": dict(v=None), "K alignment": dict(k=A + 8), "token stride": dict(stride_t=64),
