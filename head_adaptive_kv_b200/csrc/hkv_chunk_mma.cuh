@@ -17,7 +17,8 @@
 // behind 8192, Hq 32, Hkv 8, D 128: 1.61 ms without turns, 1.43 with; taking
 // part of the exponentials on the FMA units made it 1.45 to 1.53, scores in
 // half tiles of 64 keys, two in flight, 1.53: narrow products cost as much as
-// wide ones). The weights go out in halves, so that the product with V begins
+// wide ones; at D = 64, P in columns of its own, so that scores need not wait
+// for products, changed nothing). The weights go out in halves, so that the product with V begins
 // before the last of them. At that size the card is at its power limit (1.64
 // GHz); 1.15 of the 1.38 PFLOP/s that a library product sustains there.
 //
@@ -93,7 +94,6 @@ __device__ __forceinline__ bool cm_tail(const ChunkWalk<CmLine> &it)
 }
 
 // ---- loads (warps 8 and 10) ---------------------------------------------------------------
-
 //
 // A tile's boxes (a page's rows by 64 columns) are issued by two warps in
 // turn: a small box costs its issuer about as much as a large one.

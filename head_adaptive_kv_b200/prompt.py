@@ -7,6 +7,7 @@ Argument checks and marshalling only, as in ``hkv``; lengths stay on the device.
 from __future__ import annotations
 
 import ctypes as C
+import struct
 from contextlib import nullcontext
 from dataclasses import dataclass
 from functools import lru_cache
@@ -80,10 +81,10 @@ def _int32(t: torch.Tensor, n: int, what: str):
 
 
 def _together(device: int, *tensors):
-    """Every tensor on `device` (a number, as get_device gives it)."""
+    """Every tensor (and workspace) on `device` (a number, as get_device gives it)."""
     for t in tensors:
         if t is not None and t.get_device() != device:
-            raise ValueError(f"tensors on different devices ({t.device})")
+            raise ValueError(f"on different devices: {device} and {t.get_device()}")
 
 
 @lru_cache(maxsize=256)
@@ -130,6 +131,9 @@ class StatusWorkspace:
         self.device = self.tensor.get_device()
         self.ptr = self.tensor.data_ptr()
         self.init()
+
+    def get_device(self) -> int:
+        return self.device
 
     def init(self, stream=None):
         """Zero the workspace (again after a timeout)."""
@@ -319,7 +323,7 @@ def page_release(done: torch.Tensor, state: PageState, after: PageState, ws: Sta
     _int32(done, B, "done")
     state._same_pool(after)
     dev = state._device
-    _together(dev, done, ws.tensor)
+    _together(dev, done, ws)
     _call(lib.hkv_page_release, dev, stream, B, done.data_ptr(), state._pages_ref, state._ref, after._ref, ws.ptr,
           ws.nbytes)
 
@@ -376,7 +380,7 @@ def qk_norm_rope(prob: Problem, q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
             raise ValueError("give pages and slot, or k_out and v_out")
         _contiguous(k_out, dtype, (T, prob.Hkv, D), "k_out")
         _contiguous(v_out, dtype, (T, prob.Hkv, D), "v_out")
-    _together(dev, k, v, pos, rope.inv_freq, q_out, q_weight, k_weight, k_out, v_out, slot, ws.tensor)
+    _together(dev, k, v, pos, rope.inv_freq, q_out, q_weight, k_weight, k_out, v_out, slot, ws)
     _call(lib.hkv_qk_norm_rope, dev, stream, _problem(prob), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T,
           pos.data_ptr(), _p(slot), rope._ref, _p(q_weight), _p(k_weight), eps, q_out.data_ptr(), _p(k_out), _p(v_out),
           None if pages is None else pages._ref, ws.ptr, ws.nbytes)
@@ -397,21 +401,30 @@ def chunk_attention(prob: Problem, q: torch.Tensor, q_start: torch.Tensor, kv_le
     if lse is not None:
         _contiguous(lse, torch.float32, (T, prob.Hq), "lse")
     dev = pages._device
-    _together(dev, q, q_start, kv_len, out, lse, ws.tensor)
+    _together(dev, q, q_start, kv_len, out, lse, ws)
     _call(lib.hkv_chunk_attention, dev, stream, _problem(prob), q.data_ptr(), qs, T, q_start.data_ptr(),
           kv_len.data_ptr(), pages._ref, out.data_ptr(), _p(lse), ws.ptr, ws.nbytes)
 
 
-def _tier_c(t: Optional[Tier], prob: Problem, what: str):
+_TIER = struct.Struct("PPqqqiP")  # hkv_tier
+
+
+def _tier(t: Optional[Tier], prob: Problem, device: int, what: str):
+    """hkv_tier of a tier of the problem, as bytes."""
     if t is None:
         return None
-    if t.k.dtype != prob.dtype:
-        raise TypeError(f"{what}: tier of another type than the problem's")
-    _need(t.v is not None and t.v.dtype == prob.dtype, f"{what}: the tier needs V of the problem's type")
-    _need(t.k.shape[0] == prob.B and t.k.shape[1] == prob.Hkv and t.k.shape[3] == prob.D,
-          f"{what} must be [B, Hkv, cap, D] of the problem")
-    _int32(t.len, prob.units, f"{what} lengths")
-    return C.byref(t.c())
+    k, v, n = t.k, t.v, t.len
+    if v is None or k.dtype is not prob.dtype or v.dtype is not prob.dtype:
+        raise TypeError(f"{what}: the tier needs K and V of the problem's type")
+    shape, s = k.shape, k.stride()
+    if len(shape) != 4 or shape[0] != prob.B or shape[1] != prob.Hkv or shape[3] != prob.D or s[3] != 1:
+        raise ValueError(f"{what} must be [B, Hkv, cap, D] of the problem with D contiguous")
+    if v.shape != shape or v.stride() != s:
+        raise ValueError(f"{what}: K and V must share shape and strides")
+    _int32(n, prob.B * prob.Hkv, what)
+    if k.get_device() != device or v.get_device() != device or n.get_device() != device:
+        raise ValueError(f"{what}: tier on another device")
+    return _TIER.pack(k.data_ptr(), v.data_ptr(), s[0], s[1], s[2], shape[2], n.data_ptr())
 
 
 def fill_tiers(prob: Problem, pages: Pages, kv_len: torch.Tensor, dense: Optional[Tier], head: Optional[torch.Tensor],
@@ -423,13 +436,11 @@ def fill_tiers(prob: Problem, pages: Pages, kv_len: torch.Tensor, dense: Optiona
     _int32(kv_len, prob.B, "kv_len")
     if take is not None:
         _int32(take, prob.B, "take")
-    for t, what in ((head, "head"), (dropped, "dropped")):
-        if t is not None:
-            _int32(t, prob.units, what)
+    if head is not None:
+        _int32(head, prob.units, "head")
+    if dropped is not None:
+        _int32(dropped, prob.units, "dropped")
     dev = pages._device
-    for t in (dense, sparse):
-        if t is not None:
-            _together(dev, t.k, t.v, t.len)
-    _together(dev, kv_len, take, head, dropped, ws.tensor)
+    _together(dev, kv_len, take, head, dropped, ws)
     _call(lib.hkv_fill_tiers, dev, stream, _problem(prob), pages._ref, kv_len.data_ptr(), _p(take),
-          _tier_c(dense, prob, "dense"), _p(head), _tier_c(sparse, prob, "sparse"), _p(dropped), ws.ptr, ws.nbytes)
+          _tier(dense, prob, dev, "dense"), _p(head), _tier(sparse, prob, dev, "sparse"), _p(dropped), ws.ptr, ws.nbytes)
