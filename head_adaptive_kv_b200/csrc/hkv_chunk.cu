@@ -53,14 +53,15 @@ __global__ void __launch_bounds__(FC_NT, 2) k_chunk_fma(const __grid_constant__ 
     for (ChunkWalk<FcLine> it(P, sm.share); it.item(); it.next()) {
         if (!it.mine())
             continue;
+        cp_async_wait_all();
         __syncthreads();  // the item before is done with q
         for (int i = tid; i < M * (D / 4); i += FC_NT) {
             const int r = i / (D / 4), x = i % (D / 4);
-            float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < it.rows)
-                val = *reinterpret_cast<const float4 *>(P.q + (it.row0 + (r >> P.g_log2)) * P.qs +
-                                                        ((int64_t)(it.h * G + (r & (G - 1))) * D + 4 * x) * 4);
-            *reinterpret_cast<float4 *>(&sm.q[r][4 * x]) = val;
+                cp_async16(&sm.q[r][4 * x], P.q + (it.row0 + (r >> P.g_log2)) * P.qs +
+                                                ((int64_t)(it.h * G + (r & (G - 1))) * D + 4 * x) * 4);
+            else
+                *reinterpret_cast<float4 *>(&sm.q[r][4 * x]) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
         float mx[RT], sum[RT];
         float4 o[RT][CT];
@@ -82,22 +83,24 @@ __global__ void __launch_bounds__(FC_NT, 2) k_chunk_fma(const __grid_constant__ 
                     sm.ok[r] = p >= 0;
                     bad = bad || (p < 0 && key < it.r.kv);
                 }
-                float4 kk = make_float4(0.f, 0.f, 0.f, 0.f), vv = kk;
                 if (p >= 0) {
                     const int64_t at = row_offset(P.pages, p, it.h, key) + 16 * x;
-                    kk = *reinterpret_cast<const float4 *>(P.pages.k + at);
-                    vv = *reinterpret_cast<const float4 *>(P.pages.v + at);
+                    cp_async16(&sm.k[r][4 * x], P.pages.k + at);
+                    cp_async16(&sm.v[r][4 * x], P.pages.v + at);
+                } else {
+                    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+                    *reinterpret_cast<float4 *>(&sm.k[r][4 * x]) = none;
+                    *reinterpret_cast<float4 *>(&sm.v[r][4 * x]) = none;
                 }
-                *reinterpret_cast<float4 *>(&sm.k[r][4 * x]) = kk;
-                *reinterpret_cast<float4 *>(&sm.v[r][4 * x]) = vv;
             }
+            cp_async_wait_all();  // (the queries', too, before the first tile)
             __syncthreads();
-            float s[RT][4];
+            float2 s2[RT][4];  // even and odd elements, two products an instruction
 #pragma unroll
             for (int i = 0; i < RT; ++i)
 #pragma unroll
                 for (int n = 0; n < 4; ++n)
-                    s[i][n] = 0.0f;
+                    s2[i][n] = make_float2(0.0f, 0.0f);
 #pragma unroll 4
             for (int d = 0; d < D; d += 4) {
                 float4 a[RT], b[4];
@@ -110,10 +113,17 @@ __global__ void __launch_bounds__(FC_NT, 2) k_chunk_fma(const __grid_constant__ 
 #pragma unroll
                 for (int i = 0; i < RT; ++i)
 #pragma unroll
-                    for (int n = 0; n < 4; ++n)
-                        s[i][n] = fmaf(a[i].x, b[n].x,
-                                       fmaf(a[i].y, b[n].y, fmaf(a[i].z, b[n].z, fmaf(a[i].w, b[n].w, s[i][n]))));
+                    for (int n = 0; n < 4; ++n) {
+                        s2[i][n] = ffma2(make_float2(a[i].x, a[i].y), make_float2(b[n].x, b[n].y), s2[i][n]);
+                        s2[i][n] = ffma2(make_float2(a[i].z, a[i].w), make_float2(b[n].z, b[n].w), s2[i][n]);
+                    }
             }
+            float s[RT][4];
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    s[i][n] = s2[i][n].x + s2[i][n].y;
             int ok[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n)
@@ -166,10 +176,10 @@ __global__ void __launch_bounds__(FC_NT, 2) k_chunk_fma(const __grid_constant__ 
 #pragma unroll
                         for (int i = 0; i < RT; ++i) {
                             const float pe = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
-                            o[i][c].x = fmaf(pe, v.x, o[i][c].x);
-                            o[i][c].y = fmaf(pe, v.y, o[i][c].y);
-                            o[i][c].z = fmaf(pe, v.z, o[i][c].z);
-                            o[i][c].w = fmaf(pe, v.w, o[i][c].w);
+                            const float2 pp = make_float2(pe, pe);
+                            const float2 u = ffma2(pp, make_float2(v.x, v.y), make_float2(o[i][c].x, o[i][c].y));
+                            const float2 w2 = ffma2(pp, make_float2(v.z, v.w), make_float2(o[i][c].z, o[i][c].w));
+                            o[i][c] = make_float4(u.x, u.y, w2.x, w2.y);
                         }
                     }
             }
@@ -212,6 +222,7 @@ __global__ void __launch_bounds__(FC_NT, 2) k_chunk_fma(const __grid_constant__ 
         if (tid == 0 && !whole && it.first_part())
             P.desc[blockIdx.x] = ChunkDesc{it.parts(), it.row0, it.h, it.rows};
     }
+    cp_async_wait_all();
     if (bad)
         atomicOr(P.status, HKV_DEV_BAD_INDEX);
 }
