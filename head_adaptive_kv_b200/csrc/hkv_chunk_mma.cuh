@@ -86,11 +86,12 @@ struct RingAt {
 };
 
 // The item's last V tile holds rows behind the request's last token that take
-// part in the product (it runs over whole groups of 16 keys): their weights
-// are 0, but what lies there may be NaN.
+// part in the product (it runs over whole groups of 16 keys, of the last item
+// or of one that ends shortly before it): their weights are 0, but what lies
+// there may be NaN. Rows from the item's limit on are zeroed.
 __device__ __forceinline__ bool cm_tail(const ChunkWalk<CmLine> &it)
 {
-    return it.j1 == it.all && it.limit == it.r.kv && (it.r.kv & 15) != 0;
+    return it.j1 == it.all && ((it.limit + 15) & ~15) > it.r.kv;
 }
 
 // ---- loads (warps 8 and 10) ---------------------------------------------------------------

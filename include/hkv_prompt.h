@@ -154,9 +154,10 @@ hkv_status hkv_chunk_workspace_size(const hkv_problem *prob, int32_t tokens, siz
  *   problem's type; lse: fp32 [tokens, Hq] (natural log) or NULL. Rows behind
  *   q_start[B] are left as they are. out may not overlap q.
  * - A row that attends to nothing gives out = 0, lse = -inf.
- * - Keys and values behind kv_len, in masked tokens and in other requests' rows may hold
- *   anything, infinities and NaN included. Those of a request's own tokens
- *   have to be finite, or that request's rows of the call are undefined.
+ * - Keys and values behind kv_len and in pages that are not the request's may
+ *   hold anything, infinities and NaN included. Those of a request's own
+ *   tokens have to be finite, or that request's rows of the call are undefined
+ *   (no other request's are).
  * - q_start outside [0, tokens] or descending, or kv_len outside
  *   [0, table_cols*page], is clamped and sets HKV_DEV_LEN_CLAMPED.
  * - Sums and softmax statistics are fp32. With bf16 the weights are rounded to

@@ -130,6 +130,19 @@ def test_what_lies_behind_the_lengths_may_be_anything(dtype, page):
     c.run().check()
 
 
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_the_last_tokens_of_a_chunk_alone_in_an_item(dtype, G):
+    """The last item of the chunk is 1 to 15 tokens, and the one before ends within 16 keys of what lies behind."""
+    tokens = (256 if dtype == BF else 64) // G  # of an item
+    c = Case([(42 + i, tokens + i) for i in (1, 3, 9, 15)] + [(0, 2 * tokens + 5)], 2 * G, 2, 64, dtype, 128, seed=24)
+    for b, L in enumerate(c.kv):
+        if L % 128:
+            p = int(c.table[b, L // 128])
+            c.k[p, :, L % 128:], c.v[p, :, L % 128:] = float("nan"), float("nan")
+    c.run().check()
+
+
 def test_one_request_full_of_nan_spoils_no_other():
     lens = [(100, 5), (60, 7), (30, 1)]
     for dtype in (BF, F32):
