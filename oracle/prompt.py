@@ -11,7 +11,7 @@ import numpy as np
 
 def plan(ctx, new, held, free, count, table, page, T):
     """One request after another. Returns a dict of the state and rows after; `left` lists the requests that found no
-    room, `bad` those that are not valid."""
+    room, `bad` those that are not valid. A row whose page is not one of the pool has slot -1."""
     B, cols = table.shape
     table, held = table.copy(), [int(x) for x in held]
     want_pages = want_rows = given = rows = 0
@@ -35,7 +35,8 @@ def plan(ctx, new, held, free, count, table, page, T):
                 held[b] = h + need
         for i in range(take):
             pos.append(c + i)
-            slot.append(int(table[b, (c + i) // page]) * page + (c + i) % page)
+            p = int(table[b, (c + i) // page])
+            slot.append(p * page + (c + i) % page if 0 <= p < len(free) else -1)
         rows += take
         q_start.append(rows)
         kv_len.append(min(max(c, 0), cols * page) + take)

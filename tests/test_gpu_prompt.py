@@ -39,7 +39,8 @@ def check_plan(ctx, new, held, free, count, table, page, T, in_place=False):
         assert np.array_equal(got.cpu().numpy(), ref[name]), name
     assert int(after.free_count) == ref["count"]
     assert np.array_equal(st.free.cpu().numpy(), free)
-    assert status == (prompt.DEV_PAGES_FULL if ref["left"] else 0) | (hkv.DEV_BAD_INDEX if ref["bad"] else 0)
+    nowhere = ((ref["pos"] >= 0) & (ref["slot"] < 0)).any()  # a table entry that is no page of the pool
+    assert status == (prompt.DEV_PAGES_FULL if ref["left"] else 0) | (hkv.DEV_BAD_INDEX if ref["bad"] or nowhere else 0)
     return ref
 
 
