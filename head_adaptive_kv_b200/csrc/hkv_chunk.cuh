@@ -278,7 +278,11 @@ struct ChunkWalk {
 // starts in CTA c of the attention's grid, a warp per row, CMERGE_ROWS rows a
 // block. Lane i reads the statistics of record i (32 at a time), so a row
 // costs two round trips to memory however many parts it has. The order of
-// the sums follows from the number of records alone, not from timing.
+// the sums follows from the number of records alone, not from timing. Latency:
+// about 3 us of 16 for one token on 2000 keys. Joining in the attention's
+// kernel instead, by the CTA that finishes an item's last part, takes 1 us off
+// there but puts the join behind that CTA's other work: 2048 bf16 tokens alone
+// 66 us instead of 59, 16 fp32 tokens on 8000 keys 360 instead of 240.
 constexpr int CMERGE_NT = 256;
 constexpr int CMERGE_ROWS = 16;
 

@@ -18,9 +18,10 @@
 // part of the exponentials on the FMA units made it 1.45 to 1.53, scores in
 // half tiles of 64 keys, two in flight, 1.53: narrow products cost as much as
 // wide ones; at D = 64, P in columns of its own, so that scores need not wait
-// for products, changed nothing). The weights go out in halves, so that the product with V begins
-// before the last of them. At that size the card is at its power limit (1.64
-// GHz); 1.15 of the 1.38 PFLOP/s that a library product sustains there.
+// for products, changed nothing). The weights go out in halves, so that the
+// product with V begins before the last of them. At that size the card is at
+// its power limit (1.64 GHz): 1.09 to 1.15 of the 1.38 PFLOP/s that a library
+// product sustains there. 64 single tokens on 4k to 32k keys: 6.8 TB/s.
 //
 // Items of at most 128 rows (single tokens, short chunks) have one row tile;
 // its key tiles then go to the two softmax groups in turn, each with its own

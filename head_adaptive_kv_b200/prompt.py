@@ -299,8 +299,8 @@ def page_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, state: PageState, af
               ws: StatusWorkspace, granted: Optional[torch.Tensor] = None, stream=None):
     """Block tables, slot map and positions for new_len[b] tokens behind the ctx_len[b] cached ones of each request
     (int32 [B]; see hkv_page_plan). `after` receives the state: it shares `state`'s tables and stack, and may be
-    `state` itself, as chunk.kv_len may be ctx_len. chunk is written; granted: optional int32 [B], the tokens each request was given (0 where it was
-    left out)."""
+    `state` itself, as chunk.kv_len may be ctx_len. chunk is written; granted: optional int32 [B], the tokens each
+    request was given (0 where it was left out)."""
     B = state._rows
     _int32(ctx_len, B, "ctx_len")
     _int32(new_len, B, "new_len")

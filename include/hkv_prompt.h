@@ -40,11 +40,12 @@ extern "C" {
 
 /* The page pool: K and V of page i, KV head h, row t at
  * i*stride_p + h*stride_h + t*stride_t (elements; D contiguous; 16-byte
- * aligned like a tier's rows, strides above 0 where there is more than one), and the block tables: column c of row b names
- * the page of tokens c*page .. c*page + page-1 of request b. Any other entry
- * than a page of the pool means that the tokens are not there: they are masked
- * (attention), read as zeros (fill) or not written, and HKV_DEV_BAD_INDEX is
- * set when a call meets such an entry below a request's length. */
+ * aligned like a tier's rows, strides above 0 where there is more than one),
+ * and the block tables: column c of row b names the page of tokens
+ * c*page .. c*page + page-1 of request b. Any other entry than a page of the
+ * pool means that the tokens are not there: they are masked (attention), read
+ * as zeros (fill) or not written, and HKV_DEV_BAD_INDEX is set when a call
+ * meets such an entry below a request's length. */
 typedef struct {
     void *k, *v;                           /* device */
     int64_t stride_p, stride_h, stride_t;
