@@ -408,3 +408,125 @@ def test_one_row_of_any_stride():
     wide[:, :1024] = c.q.reshape(1, 1024)
     c.q = wide[:, :1024].unflatten(1, (8, 128))
     c.run().check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_requests_that_share_pages(dtype):
+    """A prefix's pages stand in several tables, and one page twice in the same table."""
+    c = Case([(96, 3), (96, 40), (64, 1), (200, 1)], 8, 2, 128, dtype, 32, seed=24)
+    c.table[1, :3] = c.table[0, :3]
+    c.table[2, :2] = c.table[0, :2]
+    c.table[3, 1] = c.table[3, 0]
+    c.run().check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_captured_loop(dtype):
+    """Plan, norms and attention as one graph, replayed for steps of other lengths while the state and the lengths
+    advance in place, leaves the same bits as the calls one by one; the tiers of what finished come from a second
+    graph on the same workspace, with the release."""
+    Hq, Hkv, D, page, B, T, pool_pages = 8, 2, 128, 16, 4, 128, 40
+    prob = hkv.Problem(B, Hq, Hkv, D, dtype, 1.0, 0, 0)
+    gen = torch.Generator().manual_seed(25)
+    steps = [([60, 0, 5, 0], [0, 0, 0, 0]), ([1, 40, 70, 0], [0, 0, 0, 0]), ([1, 1, 1, 1], [0, 1, 0, 1]),
+             ([0, 0, 0, 0], [0, 0, 1, 0]), ([17, 9, 100, 2], [1, 0, 0, 0])]
+    rows = [torch.randn(T, (Hq + 2 * Hkv) * D, generator=gen).to(dtype).to(DEV) for _ in steps]
+    w = (1 + 0.1 * torch.randn(D, generator=gen)).to(dtype).to(DEV)
+    rope = prompt.Rope.of_base(D, 1e4, DEV)
+
+    class Loop:
+        def __init__(self):
+            self.state = prompt.PageState.allocate(B, 16, page, pool_pages, DEV)
+            self.ch = prompt.Chunk.allocate(B, T, DEV)
+            pk, pv = (torch.zeros(pool_pages, Hkv, page, D, dtype=dtype, device=DEV) for _ in range(2))
+            self.pages, self.ws = prompt.Pages(pk, pv, self.state.table), prompt.ChunkWorkspace(prob, T, DEV)
+            self.x = torch.zeros(T, (Hq + 2 * Hkv) * D, dtype=dtype, device=DEV)
+            self.new, self.done = i32([0] * B), i32([0] * B)
+            self.q, self.out = (torch.zeros(T, Hq, D, dtype=dtype, device=DEV) for _ in range(2))
+            tier = lambda n: hkv.Tier(torch.zeros(B, Hkv, n, D, dtype=dtype, device=DEV),  # noqa: E731
+                                      torch.zeros(B, Hkv, n, D, dtype=dtype, device=DEV), i32([0] * B * Hkv))
+            self.dense, self.sparse, self.head = tier(24), tier(160), i32([0] * B * Hkv)
+
+        def step(self):
+            prompt.page_plan(self.ch.kv_len, self.new, self.state, self.state, self.ch, self.ws)
+            q, k, v = (y.unflatten(1, (-1, D)) for y in self.x.split([Hq * D, Hkv * D, Hkv * D], 1))
+            prompt.qk_norm_rope(prob, q, k, v, self.ch.pos, rope, self.q, self.ws, q_weight=w, k_weight=w,
+                                pages=self.pages, slot=self.ch.slot)
+            prompt.chunk_attention(prob, self.q, self.ch.q_start, self.ch.kv_len, self.pages, self.out, self.ws)
+
+        def finish(self):
+            prompt.fill_tiers(prob, self.pages, self.ch.kv_len, self.dense, self.head, self.sparse, self.ws,
+                              take=self.done)
+            prompt.page_release(self.done, self.state, self.state, self.ws)
+            self.ch.kv_len.mul_(1 - self.done)
+
+        def results(self):
+            return [self.state.table, self.state.free, self.state.free_count, self.state.held, self.ch.q_start,
+                    self.ch.kv_len, self.ch.pos, self.ch.slot, self.q, self.out, self.pages.k, self.pages.v,
+                    self.dense.k, self.dense.v, self.dense.len, self.sparse.k, self.sparse.v, self.sparse.len, self.head]
+
+    eager, replayed = Loop(), Loop()
+    for loop in (eager, replayed):  # no requests yet: nothing moves
+        loop.step(), loop.finish()
+    torch.cuda.synchronize()
+    graphs = []
+    for call in (replayed.step, replayed.finish):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call()
+    for (new, done), x in zip(steps, rows):
+        for loop in (eager, replayed):
+            loop.new.copy_(i32(new)), loop.done.copy_(i32(done)), loop.x.copy_(x)
+        eager.step(), eager.finish()
+        graphs[0].replay(), graphs[1].replay()
+        torch.cuda.synchronize()
+        for a, b in zip(eager.results(), replayed.results()):
+            assert torch.equal(a, b)
+    assert eager.ws.status() == 0 and replayed.ws.status() == 0
+    held = [-(-n // page) for n in eager.ch.kv_len.tolist()]
+    assert eager.state.held.tolist() == held and int(eager.state.free_count) == pool_pages - sum(held)
+    assert sorted(eager.state.free[:pool_pages - sum(held)].tolist()
+                  + [p for b, h in enumerate(held) for p in eager.state.table[b, :h].tolist()]) == list(range(pool_pages))
+
+
+def test_the_whole_side_on_two_streams_at_once():
+    """Two loops of plan, norms, attention and fill, each on a stream and a workspace of its own."""
+    Hq, Hkv, D, page, B, T = 8, 2, 64, 32, 3, 300
+    prob = hkv.Problem(B, Hq, Hkv, D, BF, 1.0, 0, 0)
+    rope = prompt.Rope.of_base(D, 1e4, DEV)
+
+    def loop(seed, stream):
+        gen = torch.Generator().manual_seed(seed)
+        state, ch = prompt.PageState.allocate(B, 16, page, 48, DEV), prompt.Chunk.allocate(B, T, DEV)
+        pk, pv = (torch.zeros(48, Hkv, page, D, dtype=BF, device=DEV) for _ in range(2))
+        pages, ws = prompt.Pages(pk, pv, state.table), prompt.ChunkWorkspace(prob, T, DEV)
+        x = [torch.randn(T, h, D, generator=gen).to(BF).to(DEV) for h in (Hq, Hkv, Hkv)]
+        new = [i32(n) for n in ([120, 7, 150], [1, 1, 1], [90, 100, 1])]
+        qo, out = (torch.zeros(T, Hq, D, dtype=BF, device=DEV) for _ in range(2))
+        dense = hkv.Tier(*(torch.zeros(B, Hkv, 300, D, dtype=BF, device=DEV) for _ in range(2)), i32([0] * B * Hkv))
+        head = i32([0] * B * Hkv)
+        outs = [torch.zeros_like(out) for _ in new]
+        torch.cuda.synchronize()
+
+        def run():
+            with torch.cuda.stream(stream):
+                for n, o in zip(new, outs):
+                    prompt.page_plan(ch.kv_len, n, state, state, ch, ws)
+                    prompt.qk_norm_rope(prob, *x, ch.pos, rope, qo, ws, pages=pages, slot=ch.slot)
+                    prompt.chunk_attention(prob, qo, ch.q_start, ch.kv_len, pages, o, ws)
+                prompt.fill_tiers(prob, pages, ch.kv_len, dense, head, None, ws)
+        return run, [*outs, pk, pv, dense.k, dense.v, dense.len, head, state.table], ws
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    alone = [loop(s, torch.cuda.current_stream()) for s in (26, 27)]
+    for run, _, _ in alone:
+        run()
+        torch.cuda.synchronize()
+    together = [loop(s, st) for s, st in zip((26, 27), streams)]
+    for run, _, _ in together:
+        run()
+    torch.cuda.synchronize()
+    for (_, a, wa), (_, b, wb) in zip(alone, together):
+        assert wa.status() == 0 and wb.status() == 0
+        for p, q in zip(a, b):
+            assert torch.equal(p, q)
