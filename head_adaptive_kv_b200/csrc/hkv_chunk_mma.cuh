@@ -15,13 +15,14 @@
 // two groups take turns at their exponentials: left alone they fall into step,
 // share the exponential units and then leave them idle together (8192 tokens
 // behind 8192, Hq 32, Hkv 8, D 128: 1.61 ms without turns, 1.43 with; taking
-// part of the exponentials on the FMA units made it 1.45 to 1.53, scores in
-// half tiles of 64 keys, two in flight, 1.53: narrow products cost as much as
-// wide ones; at D = 64, P in columns of its own, so that scores need not wait
-// for products, changed nothing). The weights go out in halves, so that the
-// product with V begins before the last of them. At that size the card is at
-// its power limit (1.64 GHz): 1.09 to 1.15 of the 1.38 PFLOP/s that a library
-// product sustains there. 64 single tokens on 4k to 32k keys: 6.8 TB/s.
+// part of the exponentials on the FMA units made it 1.45 to 1.53, at D = 64
+// 1.15 to 1.17 instead of 1.13; scores in half tiles of 64 keys, two in flight,
+// 1.53: narrow products cost as much as wide ones; at D = 64, P in columns of
+// its own, so that scores need not wait for products, changed nothing). The
+// weights go out in halves, so that the product with V begins before the last
+// of them. At that size the card is at its power limit (1.64 GHz): 1.09 to 1.15
+// of the 1.38 PFLOP/s that a library product sustains there. 64 single tokens
+// on 4k to 32k keys: 6.8 TB/s.
 //
 // Items of at most 128 rows (single tokens, short chunks) have one row tile;
 // its key tiles then go to the two softmax groups in turn, each with its own

@@ -217,26 +217,4 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b)
     return d;
 }
 
-// 2^x of a pair on the FMA units, x <= 127 (below -127: 0). Cody-Waite
-// reduction to x = n + f, |f| <= 1/2 (adding 1.5 2^23 rounds to the integer n
-// and leaves it in the low bits), a polynomial of degree 5 for 2^f (minimax of
-// the relative error by Remez exchange), and n added to its exponent. Relative
-// error below 2^-22.1, as ex2.approx.
-__device__ __forceinline__ float2 ex2_fma2(float2 x)
-{
-    constexpr float BIG = 12582912.0f;
-    x.x = fmaxf(x.x, -127.0f);
-    x.y = fmaxf(x.y, -127.0f);
-    const float2 t = fadd2(x, make_float2(BIG, BIG));
-    const float2 n = fadd2(t, make_float2(-BIG, -BIG));
-    const float2 f = fadd2(x, make_float2(-n.x, -n.y));
-    float2 p = ffma2(make_float2(0x1.5c08e6p-10f, 0x1.5c08e6p-10f), f, make_float2(0x1.3d0c52p-7f, 0x1.3d0c52p-7f));
-    p = ffma2(p, f, make_float2(0x1.c6b6e4p-5f, 0x1.c6b6e4p-5f));
-    p = ffma2(p, f, make_float2(0x1.ebf918p-3f, 0x1.ebf918p-3f));
-    p = ffma2(p, f, make_float2(0x1.62e428p-1f, 0x1.62e428p-1f));
-    p = ffma2(p, f, make_float2(0x1.000002p+0f, 0x1.000002p+0f));
-    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
-                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
-}
-
 }  // namespace hkv
