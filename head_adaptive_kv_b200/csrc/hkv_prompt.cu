@@ -539,6 +539,17 @@ static hkv_status check_status_ws(const void *ws, size_t ws_bytes)
 
 static bool words(const void *p) { return p != nullptr && ptr_aligned(p, 4); }
 
+// Bytes that a call reads or writes.
+struct Span {
+    const void *p;
+    int64_t bytes;
+    bool meets(const Span &x) const
+    {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(x.p);
+        return a < b ? b - a < (uintptr_t)bytes : a - b < (uintptr_t)x.bytes;
+    }
+};
+
 hkv_status check_pages(const hkv_pages *g, const hkv_problem *p, bool storage, bool table)
 {
     if (g == nullptr || g->pages < 0 ||
@@ -709,6 +720,22 @@ hkv_status hkv_qk_norm_rope(const hkv_problem *prob, const void *q, int64_t q_st
             return HKV_ERR_INVALID_ARG;
     if (tokens > 0 && (q_out == nullptr || !ptr_aligned(q_out, 16) || !words(pos)))
         return HKV_ERR_INVALID_ARG;
+    // A CTA writes its tokens' rows while others still read theirs: an output may stand on its own input row on row,
+    // and on nothing else.
+    const Span outs[3] = {{q_out, tokens * rows[0].heads * D * es},
+                          {k_out, k_out ? tokens * rows[1].heads * D * es : 0},
+                          {v_out, v_out ? tokens * rows[2].heads * D * es : 0}};
+    for (int o = 0; o < 3 && tokens > 0; ++o) {
+        for (int i = 0; i < 3; ++i) {
+            const int64_t row = rows[i].heads * D;
+            const bool in_place = i == o && outs[o].p == rows[i].p && (tokens == 1 || rows[i].stride == row);
+            if (!in_place && outs[o].meets({rows[i].p, ((tokens - 1) * rows[i].stride + row) * es}))
+                return HKV_ERR_INVALID_ARG;
+        }
+        for (int i = 0; i < o; ++i)
+            if (outs[o].meets(outs[i]))
+                return HKV_ERR_INVALID_ARG;
+    }
     if ((s = check_status_ws(ws, ws_bytes)) != HKV_OK)
         return s;
     if (tokens == 0)

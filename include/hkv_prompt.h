@@ -125,14 +125,18 @@ typedef struct {
  * Computed in fp32, rounded once.
  * - q, k, v: device rows of [tokens, heads, D], heads and D contiguous, row
  *   strides in elements (slices of one projection's output will do), all
- *   16-byte aligned. q_out: [tokens, Hq, D] contiguous; may be q itself.
+ *   16-byte aligned. q_out: [tokens, Hq, D] contiguous.
  * - pos: device int32 [tokens]; a row with pos < 0 is skipped (its outputs are
  *   left as they are).
  * - K and V rows go to the pages at slot[row] (pages and slot given; -1 = not
  *   written; another slot outside the pool is not written either and sets
  *   HKV_DEV_BAD_INDEX; rows of one call that share a slot leave a mixture of
  *   their values in it), or to k_out, v_out [tokens, Hkv, D] contiguous (given
- *   instead; the layout of hkv_append's k_new, v_new), which may be k and v.
+ *   instead; the layout of hkv_append's k_new, v_new).
+ * - q_out may be q itself, k_out k and v_out v, where their rows are contiguous
+ *   too (stride heads*D, or one token); an output that overlaps an input in any
+ *   other way, or another output, is refused (HKV_ERR_INVALID_ARG; the input's
+ *   span counts from its first row to its last, the gaps between rows included).
  * - q_w, k_w: device [D] of the problem's type, both or neither, 16-byte
  *   aligned; eps >= 0.
  * - ws: any workspace of at least 256 bytes. B is not used. One kernel. */

@@ -130,6 +130,31 @@ def test_norm_rope_refusals(pr, hk):
     assert _norm(pr, prob, T=0) == 0  # nothing to do
 
 
+def test_norm_rope_refuses_outputs_over_rows_that_others_still_read(pr, hk):
+    """An output may stand on its own input, row on row; any other overlap would be written before it is read."""
+    prob = _prob(hk)  # 8 query and 2 KV heads of 128 in bf16: rows of 2048 and 512 bytes
+    far = 64 * A
+    at = dict(q=A, k=2 * A, v=3 * A, qo=far, ko=2 * far, vo=3 * far)
+    over = {"q in place, rows apart": dict(qo=A, qs=1536), "k in place, rows apart": dict(ko=2 * A, ks=512),
+            "v in place, rows apart": dict(vo=3 * A, vs=264), "q_out a row into q": dict(qo=A + 2048),
+            "q_out ends in k": dict(qo=2 * A - 5 * 2048 + 16), "k_out on v": dict(ko=3 * A),
+            "v_out on k": dict(vo=2 * A), "k_out behind the first row of q": dict(ko=A + 2048),
+            "q_out on k_out": dict(qo=2 * far), "k_out on v_out": dict(ko=3 * far),
+            "v_out ends in q_out": dict(vo=far - 5 * 512 + 16),
+            "slices of one projection, k_out on them": dict(q=A, k=A + 2048, v=A + 2560, qs=1536, ks=1536, vs=1536, ko=A + 4096)}
+    for what, kw in over.items():
+        assert _norm(pr, prob, **{**at, **kw}) == 1, what
+    assert _norm(pr, prob, **{**at, "qo": A, "qs": 1536}, pages=_pages(pr), slot=A) == 1  # rows and pages besides
+    paged = dict(at, ko=None, vo=None, pages=_pages(pr), slot=A)
+    assert _norm(pr, prob, **{**paged, "qo": A, "qs": 1536}) == 1
+    assert _norm(pr, prob, **{**paged, "qo": 3 * A}) == 1
+    # what is allowed gets as far as the workspace: in place, one row of any stride, neighbours that touch
+    allowed = [dict(), dict(qo=A), dict(qo=A, ko=2 * A, vo=3 * A), dict(T=1, qo=A, qs=1536, ko=2 * A, ks=512),
+               dict(qo=A + 5 * 2048), dict(ko=2 * A - 5 * 512), dict(q=A, k=A + 2048, v=A + 2560, qs=1536, ks=1536, vs=1536)]
+    for kw in allowed:
+        assert _norm(pr, prob, ws=None, **{**at, **kw}) == 6, kw
+
+
 def _attn(pr, prob, q=A, qs=1024, T=5, q_start=A, kv=A, pages=None, out=2 * A, lse=None, ws=A, nbytes=1 << 30):
     g = _pages(pr) if pages is None else pages
     return pr.lib.hkv_chunk_attention(C.byref(prob.c()), q, qs, T, q_start, kv, C.byref(g), out, lse, ws, nbytes, None)
