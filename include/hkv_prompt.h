@@ -104,7 +104,8 @@ hkv_status hkv_page_plan(int32_t B, const int32_t *ctx_len, const int32_t *new_l
  * keeps its entries, which then mean nothing). States as for hkv_page_plan,
  * but this call writes `free` above free_count. A state that does not fit the pool
  * (a held count below 0 or above the table's columns, more pages than the
- * stack has room for) sets HKV_DEV_BAD_INDEX and releases nothing. */
+ * stack has room for, a table entry to go back that is no page of the pool) sets
+ * HKV_DEV_BAD_INDEX and releases nothing. */
 hkv_status hkv_page_release(int32_t B, const int32_t *done, const hkv_pages *pages, const hkv_page_state *in,
                             const hkv_page_state *after, void *ws, size_t ws_bytes, hkv_stream_t stream);
 

@@ -171,6 +171,34 @@ def test_release_of_a_state_that_does_not_fit():
         assert st.held.tolist() == held and st.free_count.tolist() == [count] and torch.equal(st.free, free)
 
 
+@pytest.mark.parametrize("B", [3, 200])  # one CTA's share of the requests, and several
+@pytest.mark.parametrize("entry", [-1, -2**31, 2**31 - 1, "pages"])
+def test_release_of_entries_that_are_no_pages(B, entry):
+    """A table entry that names no page of the pool must not reach the stack, where it would be given out again: the
+    whole release is refused, and one without the request that holds the entry goes through."""
+    page, cols = 16, 3
+    st = prompt.PageState.allocate(B, cols, page, B * cols, DEV)
+    ws, ch = prompt.status_workspace(DEV), prompt.Chunk.allocate(B, B * cols * page, DEV)
+    prompt.page_plan(i32([0] * B), i32([cols * page] * B), st, st, ch, ws)
+    assert ws.status() == 0 and int(st.free_count) == 0
+    bad = B - 2  # its last column, as far as a page number goes
+    st.table[bad, cols - 1] = B * cols if entry == "pages" else entry
+    st.free.fill_(-9)
+    before = [x.clone() for x in (st.table, st.free, st.free_count, st.held)]
+    after = prompt.PageState(st.table, st.free, i32([-7]), i32([-7] * B), page, B * cols)
+    prompt.page_release(i32([1] * B), st, after, ws)
+    assert ws.status() == hkv.DEV_BAD_INDEX
+    assert int(after.free_count) == 0 and after.held.tolist() == [cols] * B
+    for x, y in zip((st.table, st.free, st.free_count, st.held), before):
+        assert torch.equal(x, y)
+    done = np.ones(B, np.int32)
+    done[bad] = 0
+    free, count, held = op.release(done, st.held.cpu().numpy(), st.free.cpu().numpy(), 0, st.table.cpu().numpy())
+    prompt.page_release(i32(done), st, st, ws)
+    assert ws.status() == 0 and int(st.free_count) == count
+    assert np.array_equal(st.free.cpu().numpy(), free) and np.array_equal(st.held.cpu().numpy(), held)
+
+
 # ---- norms and rotation ---------------------------------------------------------
 
 
