@@ -102,7 +102,7 @@ __device__ __forceinline__ bool cm_tail(const ChunkWalk<CmLine> &it)
 // turn: a small box costs its issuer about as much as a large one.
 
 template <int D>
-__device__ __forceinline__ void cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const Ctl &c, int lane, const int w)
+__device__ __forceinline__ bool cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const uint32_t limit, int lane, const int w)
 {
     using SM = CmSmem<D>;
     const ChunkP &A = P.c;
@@ -112,9 +112,9 @@ __device__ __forceinline__ void cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const
     const uint32_t box = (uint32_t)rows * 128;             // bytes of a box
     RingAt<SM::NST> at;
     uint32_t items = 0, issued = 0;
-    bool bad = false;
+    bool ok = true, bad = false;
     if (A.withhold)
-        return;
+        return true;
     for (ChunkWalk<CmLine> it(A, sm.share); it.item(); it.next()) {
         const int n = it.j1 - it.j0;
         if (n <= 0)
@@ -128,7 +128,8 @@ __device__ __forceinline__ void cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const
             return __ldg(G.table + it.b * G.table_stride + (key >> G.page_log2));
         };
         int next_k = page(0);
-        if (!mbar_await(&sm.q_empty, (items & 1) ^ 1, c))
+        ok = mbar_await(&sm.q_empty, (items & 1) ^ 1, limit);
+        if (!ok)
             break;
         if (elect_one()) {
             const int tiles = it.rows <= 128 ? 1 : 2, toks = 128 >> A.g_log2;
@@ -147,7 +148,6 @@ __device__ __forceinline__ void cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const
         __syncwarp();
         ++items;
         // the ring's order: K0 V0 K1 V1 ..., or with one row tile K0 K1 V0 K2 V1 ...
-        bool ok = true;
         int kj = 0, page0 = -1, page1 = -1;  // the pages of tiles vj and vj + 1
         for (int vj = 0; vj < n && ok;) {
             const bool is_k = kj < min(n, vj + ahead);
@@ -159,10 +159,9 @@ __device__ __forceinline__ void cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const
                 page0 = page1;
                 ++vj;
             }
-            if (!mbar_await(&sm.empty[at.i], at.phase ^ 1, c)) {
-                ok = false;
+            ok = mbar_await(&sm.empty[at.i], at.phase ^ 1, limit);
+            if (!ok)
                 break;
-            }
             uint64_t *bar = &sm.full[at.i];
             const int boxes = min(per, (it.limit - (it.j0 + j) * CM_NK + rows - 1) / rows);
             const bool lead = elect_one(), there = entry >= 0 && entry < G.pages;
@@ -187,8 +186,8 @@ __device__ __forceinline__ void cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const
             break;
     }
     if (bad)
-        raise_flag(c, HKV_DEV_BAD_INDEX);
-    if (timed_out(c)) {
+        atomicOr(A.status, HKV_DEV_BAD_INDEX);
+    if (!ok || timed_out(Ctl{A.status, A.wait_ns})) {
         // let what is on its way land before the CTA ends
         RingAt<SM::NST> back = at;
         for (int i = 0; i < SM::NST && (uint32_t)i < issued; ++i) {
@@ -202,6 +201,7 @@ __device__ __forceinline__ void cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const
         if (items > 0)
             mbar_let_land(&sm.q_full, (items - 1) & 1);
     }
+    return ok;
 }
 
 // ---- matrix instructions (warps 9 and 11, one per softmax group) --------------------------
@@ -211,7 +211,7 @@ __device__ __forceinline__ void cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const
 // which one lane runs alone, could not keep the tensor cores fed.
 
 template <int D>
-__device__ __forceinline__ bool cm_issue(const ChunkMmaP &P, CmSmem<D> &sm, const Ctl &c, const int g)
+__device__ __forceinline__ bool cm_issue(const ChunkMmaP &P, CmSmem<D> &sm, const uint32_t limit, const int g)
 {
     using SM = CmSmem<D>;
     constexpr uint32_t ID_S = mma_idesc(CM_NK, false), ID_O = mma_idesc(D, true);
@@ -219,7 +219,7 @@ __device__ __forceinline__ bool cm_issue(const ChunkMmaP &P, CmSmem<D> &sm, cons
     const uint32_t ring = mma_low(smem_addr(sm.ring[0]), 0), q0 = mma_low(smem_addr(sm.q[0]), 16);
     RingAt<SM::NST> at;
     uint32_t items = 0, p_count = 0;
-    const auto landed = [&]() { return mbar_await(&sm.full[at.i], at.phase, c); };
+    const auto landed = [&]() { return mbar_await(&sm.full[at.i], at.phase, limit); };
     // Both warps go past every stage and both free it (a parity wait that
     // skips phases, or one that a faster warp leaves two phases behind, would
     // be answered for the wrong one).
@@ -267,7 +267,7 @@ __device__ __forceinline__ bool cm_issue(const ChunkMmaP &P, CmSmem<D> &sm, cons
             for (int s = from; s < to_step; ++s)
                 mma_ts(to, ts + s * 8, v + s * (2048 >> 4), ID_O, !(first && s == 0));
         };
-        if (!mbar_await(&sm.p_half[g], p_count & 1, c))
+        if (!mbar_await(&sm.p_half[g], p_count & 1, limit))
             return false;
         tc_fence_after();
         if (elect_one()) {
@@ -281,7 +281,7 @@ __device__ __forceinline__ bool cm_issue(const ChunkMmaP &P, CmSmem<D> &sm, cons
             }
         }
         __syncwarp();
-        if (!mbar_await(&sm.p_full[g], p_count & 1, c))
+        if (!mbar_await(&sm.p_full[g], p_count & 1, limit))
             return false;
         ++p_count;
         tc_fence_after();
@@ -313,7 +313,7 @@ __device__ __forceinline__ bool cm_issue(const ChunkMmaP &P, CmSmem<D> &sm, cons
         const bool one = it.rows <= 128;
         const auto keys = [&](int j) { return it.limit - (it.j0 + j) * CM_NK; };  // from tile j on
         const bool tail = cm_tail(it);
-        if (!mbar_await(&sm.q_full, items & 1, c))
+        if (!mbar_await(&sm.q_full, items & 1, limit))
             return false;
         ++items;
         if (one) {
@@ -381,7 +381,7 @@ __device__ __forceinline__ bool cm_issue(const ChunkMmaP &P, CmSmem<D> &sm, cons
 // ---- softmax and output (warps 0-7) -----------------------------------------------------
 
 template <int D>
-__device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, const Ctl &c)
+__device__ __forceinline__ bool cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, const uint32_t limit)
 {
     const ChunkP &A = P.c;
     const int tid = threadIdx.x, group = tid / 128, row = tid % 128, lane = tid & 31, warp = row / 32;
@@ -410,8 +410,8 @@ __device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, co
                 const int key = key0 + (lane & 7) * 16;
                 holes = __ballot_sync(0xffffffffu, key < it.limit && page_of(A.pages, it.b, key) < 0) & 0xffu;
             }
-            if (!mbar_await(&sm.s_full[group], s_count & 1, c))
-                return;
+            if (!mbar_await(&sm.s_full[group], s_count & 1, limit))
+                return false;
             ++s_count;
             if (warp_on) {
                 tc_fence_after();
@@ -479,8 +479,8 @@ __device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, co
                         w[e / 2] = *reinterpret_cast<const uint32_t *>(&b);
                     }
                 };
-                if (!one && !mbar_await(&sm.turn[group][warp], (turns & 1) ^ (group == 0), c))
-                    return;
+                if (!one && !mbar_await(&sm.turn[group][warp], (turns & 1) ^ (group == 0), limit))
+                    return false;
                 uint32_t w[32];
                 weigh(0, w);
                 weigh(1, w + 16);
@@ -501,8 +501,8 @@ __device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, co
                 tc_fence_before();
                 __syncwarp();
             } else {
-                if (!one && !mbar_await(&sm.turn[group][warp], (turns & 1) ^ (group == 0), c))
-                    return;
+                if (!one && !mbar_await(&sm.turn[group][warp], (turns & 1) ^ (group == 0), limit))
+                    return false;
                 if (lane == 0) {
                     mbar_arrive(&sm.p_half[group]);
                     if (!one)
@@ -517,8 +517,8 @@ __device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, co
         // the item's output (group 1 of a single row tile hands its part to group 0)
         const bool mine = begun;
         if (mine) {
-            if (!mbar_await(&sm.o_full[group], o_count & 1, c))
-                return;
+            if (!mbar_await(&sm.o_full[group], o_count & 1, limit))
+                return false;
             ++o_count;
         }
         if (!one && n > 0)
@@ -528,8 +528,8 @@ __device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, co
             sm.xm[row] = m;
             sm.xl[row] = l;
             mbar_arrive(&sm.x_ready);
-            if (!mbar_await(&sm.x_done, x_count & 1, c))
-                return;
+            if (!mbar_await(&sm.x_done, x_count & 1, limit))
+                return false;
             ++x_count;
             continue;
         }
@@ -537,8 +537,8 @@ __device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, co
             continue;
         float fa = 1.0f, fb = 0.0f;
         if (two_parts) {
-            if (!mbar_await(&sm.x_ready, x_count & 1, c) || !mbar_await(&sm.o_full[1], o_other & 1, c))
-                return;
+            if (!mbar_await(&sm.x_ready, x_count & 1, limit) || !mbar_await(&sm.o_full[1], o_other & 1, limit))
+                return false;
             ++x_count;
             ++o_other;
             const float m1 = sm.xm[row], l1 = sm.xl[row], M = fmaxf(m, m1), base = M == -INFINITY ? 0.0f : M;
@@ -651,6 +651,7 @@ __device__ __forceinline__ void cm_softmax(const ChunkMmaP &P, CmSmem<D> &sm, co
         if (tid == 0 && !whole && it.first_part())
             A.desc[blockIdx.x] = ChunkDesc{it.parts(), it.row0, it.h, it.rows};
     }
+    return true;
 }
 
 template <int D>
@@ -689,7 +690,7 @@ __global__ void __launch_bounds__(CM_NT, 1) k_chunk_mma(const __grid_constant__ 
         reinterpret_cast<uint4 *>(sm.q[0])[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     wait_prior_grid();
-    const Ctl c{P.c.status, P.c.wait_ns};
+    const uint32_t limit = await_limit(P.c.wait_ns);
     if (tid == 0)
         P.c.desc[blockIdx.x].n = 0;
     tc_fence_before();
@@ -697,19 +698,26 @@ __global__ void __launch_bounds__(CM_NT, 1) k_chunk_mma(const __grid_constant__ 
     __syncthreads();
     tc_fence_after();
     // the launch's 384 x 168 registers, as 256 x 208 + 128 x 88: a softmax thread holds a row of S
+    bool through;  // no wait of this warp has run out
     if (warp < 8) {
         regs_take<208>();
-        cm_softmax<D>(P, sm, c);
+        through = cm_softmax<D>(P, sm, limit);
     } else {
         regs_give<88>();
         if (warp == 8 || warp == 10) {
-            cm_load<D>(P, sm, c, lane, warp == 10);
-        } else if (const int g = warp == 11; !cm_issue<D>(P, sm, c, g)) {
-            if (elect_one())
-                mma_commit(&sm.drained[g]);
-            mbar_let_land(&sm.drained[g], 0);
+            through = cm_load<D>(P, sm, limit, lane, warp == 10);
+        } else {
+            const int g = warp == 11;
+            through = cm_issue<D>(P, sm, limit, g);
+            if (!through) {
+                if (elect_one())
+                    mma_commit(&sm.drained[g]);
+                mbar_let_land(&sm.drained[g], 0);
+            }
         }
     }
+    if (!through)
+        atomicOr(P.c.status, HKV_DEV_TIMEOUT);
     tc_fence_before();
     __syncthreads();
     if (warp == 9) {

@@ -10,26 +10,33 @@ namespace hkv {
 // As mbar_wait and mbar_wait_bounded, but inlined: a kernel that moves
 // registers between its warps cannot call functions.
 
-__device__ __forceinline__ bool mbar_await(uint64_t *bar, uint32_t parity, const Ctl &c)
+// The low word of the global timer (ns): differences below 2^32 count.
+__device__ __forceinline__ uint32_t global_ns_low()
 {
-    // the clock and the status word are slow to read beside a wait of a
-    // thousand cycles: looked at only once the wait is a long one
-    uint64_t t0 = 0;
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity))
-            return true;
-        if ((it & 1023u) == 0) {
-            const uint64_t now = global_ns();
-            if (t0 == 0)
-                t0 = now;
-            if (timed_out(c))
-                return false;
-            if (now - t0 > c.wait_ns) {
-                raise_flag(c, HKV_DEV_TIMEOUT);
-                return false;
-            }
-        }
-    }
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+
+// The bound of a wait as mbar_await takes it: 2^31 ns at most.
+__device__ __forceinline__ uint32_t await_limit(uint64_t wait_ns) { return (uint32_t)min(wait_ns, (uint64_t)1 << 31); }
+
+// For a whole warp, which goes on together or gives up together: the votes,
+// elections and .aligned instructions behind a wait need all of its lanes, and
+// a lane that saw the limit pass a poll before the others would leave them
+// standing there for good. Whoever gives up raises HKV_DEV_TIMEOUT, outside.
+// Short on purpose, as it stands in many places of a kernel whose code is too
+// long to stay close: 256 single tokens on 100 to 500 keys (pages of 16) take
+// 119 us so, 140 with the flag raised and the status word looked at here.
+__device__ __forceinline__ bool mbar_await(uint64_t *bar, uint32_t parity, uint32_t limit)
+{
+    const uint32_t t0 = global_ns_low();
+    bool ok;
+#pragma unroll 1
+    do
+        ok = mbar_try_wait(bar, parity);
+    while (!ok && global_ns_low() - t0 <= limit);
+    return __all_sync(0xffffffffu, ok);
 }
 
 __device__ __forceinline__ void mbar_let_land(uint64_t *bar, uint32_t parity)

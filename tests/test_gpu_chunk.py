@@ -530,3 +530,29 @@ def test_the_whole_side_on_two_streams_at_once():
         assert wa.status() == 0 and wb.status() == 0
         for p, q in zip(a, b):
             assert torch.equal(p, q)
+
+
+# one row tile whose key tiles go to both groups, one with a single key tile, two row tiles, and a mixture over many CTAs
+KINDS = {"one": [(900, 1)], "short": [(20, 3)], "two": [(700, 200)], "all": [(900, 1), (20, 3), (700, 200), (5000, 90)] * 12}
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", KINDS.values(), ids=KINDS)
+def test_warps_give_up_as_one(lens, D):
+    """Loads withheld, with limits from less than a poll of the clock to some hundred of them, so that lanes of a warp may
+    see the limit pass at different polls: the kernel ends every time and the next call after a new start is right."""
+    c = Case(lens, 8, 2, D, BF, 32, seed=29)
+    for limit in (1, 3000, 50_000, 400_000):
+        hkv.set_wait_limit_ns(limit)
+        hkv.debug_withhold_publish(True)
+        try:
+            for _ in range(3):
+                c.run()
+            torch.cuda.synchronize()
+        finally:
+            hkv.debug_withhold_publish(False)
+            hkv.set_wait_limit_ns(1_000_000_000)
+        assert c.ws.status() == hkv.DEV_TIMEOUT
+        c.ws.init()
+    c.out.fill_(5.0), c.lse.fill_(5.0)
+    c.run().check()
