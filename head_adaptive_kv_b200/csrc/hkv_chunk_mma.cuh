@@ -66,7 +66,8 @@ struct CmSmem {
     uint64_t p_half[2], p_full[2];  // the weights of the tile's first 64 keys, of all
     uint64_t turn[2][4];            // a warp's exponentials may begin: the other group's warp beside it is through
     uint64_t x_ready, x_done;  // one row tile: group 1's statistics are there / its O has been read
-    uint64_t drained[2];       // after a failed wait: the matrix instructions issued are done
+    uint64_t drained[2];       // after a wait that ran out: the matrix instructions issued are done
+    uint32_t items[2], issued[2];  // whose Q, and stages of the ring, a load warp has asked for
     uint32_t tmem;
     ChunkShare share;
     unsigned long long red[CM_NT / 32];
@@ -113,6 +114,8 @@ __device__ __forceinline__ bool cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const
     RingAt<SM::NST> at;
     uint32_t items = 0, issued = 0;
     bool ok = true, bad = false;
+    if (lane == 0)
+        sm.items[w] = sm.issued[w] = 0;
     if (A.withhold)
         return true;
     for (ChunkWalk<CmLine> it(A, sm.share); it.item(); it.next()) {
@@ -187,19 +190,9 @@ __device__ __forceinline__ bool cm_load(const ChunkMmaP &P, CmSmem<D> &sm, const
     }
     if (bad)
         atomicOr(A.status, HKV_DEV_BAD_INDEX);
-    if (!ok || timed_out(Ctl{A.status, A.wait_ns})) {
-        // let what is on its way land before the CTA ends
-        RingAt<SM::NST> back = at;
-        for (int i = 0; i < SM::NST && (uint32_t)i < issued; ++i) {
-            if (back.i == 0) {
-                back.i = SM::NST;
-                back.phase ^= 1;
-            }
-            --back.i;
-            mbar_let_land(&sm.full[back.i], back.phase);
-        }
-        if (items > 0)
-            mbar_let_land(&sm.q_full, (items - 1) & 1);
+    if (lane == 0) {
+        sm.items[w] = items;
+        sm.issued[w] = issued;
     }
     return ok;
 }
@@ -704,22 +697,34 @@ __global__ void __launch_bounds__(CM_NT, 1) k_chunk_mma(const __grid_constant__ 
         through = cm_softmax<D>(P, sm, limit);
     } else {
         regs_give<88>();
-        if (warp == 8 || warp == 10) {
+        if (warp == 8 || warp == 10)
             through = cm_load<D>(P, sm, limit, lane, warp == 10);
-        } else {
-            const int g = warp == 11;
-            through = cm_issue<D>(P, sm, limit, g);
-            if (!through) {
-                if (elect_one())
-                    mma_commit(&sm.drained[g]);
-                mbar_let_land(&sm.drained[g], 0);
-            }
-        }
+        else
+            through = cm_issue<D>(P, sm, limit, warp == 11);
     }
-    if (!through)
-        atomicOr(P.c.status, HKV_DEV_TIMEOUT);
     tc_fence_before();
-    __syncthreads();
+    if (!__syncthreads_and(through)) {
+        // Somebody's wait has run out, so not all that is under way has been waited for, not even by warps that came
+        // through: loads, products and weights land before the CTA ends.
+        if (tid == 0)
+            atomicOr(P.c.status, HKV_DEV_TIMEOUT);
+        if (warp < 8) {
+            tmem_wait_st();
+        } else if (warp == 8 || warp == 10) {
+            constexpr uint32_t NST = CmSmem<D>::NST;
+            const uint32_t items = sm.items[warp == 10], issued = sm.issued[warp == 10];
+            for (uint32_t i = issued < NST ? 0 : issued - NST; i < issued; ++i)
+                mbar_let_land(&sm.full[i % NST], (i / NST) & 1);
+            if (items > 0)
+                mbar_let_land(&sm.q_full, (items - 1) & 1);
+        } else {
+            if (elect_one())
+                mma_commit(&sm.drained[warp == 11]);
+            mbar_let_land(&sm.drained[warp == 11], 0);
+        }
+        tc_fence_before();
+        __syncthreads();
+    }
     if (warp == 9) {
         tc_fence_after();
         tmem_free(sm.tmem, 512);

@@ -39,10 +39,11 @@ __device__ __forceinline__ bool mbar_await(uint64_t *bar, uint32_t parity, uint3
     return __all_sync(0xffffffffu, ok);
 }
 
+// A millisecond at most, whatever the limit: what was started before this lands.
 __device__ __forceinline__ void mbar_let_land(uint64_t *bar, uint32_t parity)
 {
-    const uint64_t t0 = global_ns();
-    while (!mbar_try_wait(bar, parity) && global_ns() - t0 < 1000000ull) {
+    const uint32_t t0 = global_ns_low();
+    while (!mbar_try_wait(bar, parity) && global_ns_low() - t0 < 1000000u) {
     }
 }
 

@@ -556,3 +556,28 @@ def test_warps_give_up_as_one(lens, D):
         c.ws.init()
     c.out.fill_(5.0), c.lse.fill_(5.0)
     c.run().check()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", KINDS.values(), ids=KINDS)
+def test_limits_that_pass_in_the_middle(lens, D):
+    """Nothing is withheld, but the waits' limit is short, so that any of them may run out while loads and products are
+    under way: the kernel lets them land and ends, the status word says so, or the results are right."""
+    c = Case(lens, 8, 2, D, BF, 32, seed=30)
+    ref = c.reference()
+    c.reference = lambda: ref
+    for limit in (1, 300, 1000, 3000, 10_000, 30_000, 100_000):
+        hkv.set_wait_limit_ns(limit)
+        try:
+            c.out.fill_(5.0), c.lse.fill_(5.0)
+            c.run()
+            torch.cuda.synchronize()
+        finally:
+            hkv.set_wait_limit_ns(1_000_000_000)
+        status = c.ws.status()
+        assert status in (0, hkv.DEV_TIMEOUT)
+        c.ws.init()
+        if status == 0:
+            c.check()
+    c.out.fill_(5.0), c.lse.fill_(5.0)
+    c.run().check()
