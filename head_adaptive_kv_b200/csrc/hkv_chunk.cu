@@ -558,6 +558,12 @@ hkv_status hkv_chunk_attention(const hkv_problem *prob, const void *q, int64_t q
         return HKV_ERR_INVALID_ARG;
     if (!ptr_aligned(lse, 4))
         return HKV_ERR_INVALID_ARG;
+    if (tokens > 0) {
+        const Span rows{q, ((tokens - 1) * q_stride + (int64_t)prob->Hq * D) * es};
+        const Span o{out, (int64_t)tokens * prob->Hq * D * es}, l{lse, lse ? (int64_t)tokens * prob->Hq * 4 : 0};
+        if (o.meets(rows) || l.meets(rows) || l.meets(o))
+            return HKV_ERR_INVALID_ARG;
+    }
     const ChunkWs w = chunk_ws(prob, tokens);
     if (ws == nullptr || !ptr_aligned(ws, 256) || ws_bytes < w.total)
         return HKV_ERR_WORKSPACE;

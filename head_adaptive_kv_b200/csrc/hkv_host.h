@@ -28,6 +28,17 @@ hkv_status prepare(const void *fn, int threads, size_t smem, int *blocks_per_sm)
 
 inline bool ptr_aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Bytes that a call reads or writes.
+struct Span {
+    const void *p;
+    int64_t bytes;
+    bool meets(const Span &x) const
+    {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(x.p);
+        return a < b ? b - a < (uintptr_t)bytes : a - b < (uintptr_t)x.bytes;
+    }
+};
+
 // Launch `kernel` as a programmatic dependent of the previous kernel on the
 // stream (it calls wait_prior_grid() before it reads that kernel's results);
 // cluster: CTAs per cluster (1 = none).

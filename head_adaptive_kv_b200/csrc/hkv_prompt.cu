@@ -571,17 +571,6 @@ static hkv_status check_status_ws(const void *ws, size_t ws_bytes)
 
 static bool words(const void *p) { return p != nullptr && ptr_aligned(p, 4); }
 
-// Bytes that a call reads or writes.
-struct Span {
-    const void *p;
-    int64_t bytes;
-    bool meets(const Span &x) const
-    {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(x.p);
-        return a < b ? b - a < (uintptr_t)bytes : a - b < (uintptr_t)x.bytes;
-    }
-};
-
 hkv_status check_pages(const hkv_pages *g, const hkv_problem *p, bool storage, bool table)
 {
     if (g == nullptr || g->pages < 0 ||

@@ -158,7 +158,8 @@ hkv_status hkv_chunk_workspace_size(const hkv_problem *prob, int32_t tokens, siz
  * - q: device [tokens, Hq, D] rows of row stride q_stride (elements; heads and
  *   D contiguous; 16-byte aligned). out: [tokens, Hq, D] contiguous, of the
  *   problem's type; lse: fp32 [tokens, Hq] (natural log) or NULL. Rows behind
- *   q_start[B] are left as they are. out may not overlap q.
+ *   q_start[B] are left as they are. out and lse may not overlap q (its span,
+ *   gaps between rows included) or each other: HKV_ERR_INVALID_ARG.
  * - A row that attends to nothing gives out = 0, lse = -inf.
  * - Keys and values behind kv_len and in pages that are not the request's may
  *   hold anything, infinities and NaN included. Those of a request's own
