@@ -385,6 +385,20 @@ def test_many_requests(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+def test_the_most_requests(dtype):
+    """8192 requests, the limit of a call."""
+    Case([(3 * i % 50, 0 if i % 7 == 3 else 1) for i in range(8192)], 2, 2, 64, dtype, 16, seed=31).run().check()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", [[(32767, 1)], [(16384, 32)], [(20000, 1), (12000, 45), (9, 1)]], ids=lambda x: f"{len(x)}x{x[0]}")
+def test_items_in_more_parts_than_a_warp_has_lanes(lens, D):
+    """One KV head: a few items on long contexts, each cut over a hundred CTAs or so and joined 32 records at a time."""
+    for dtype in (BF, F32):
+        Case(lens, 8, 1, D, dtype, 128, seed=32).run().check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_single_tokens_in_a_batch_of_more_rows(dtype):
     """Rows above the requests' count pick the kernel for chunks; the lengths may be single tokens all the same, and
     fewer rows than requests may hold one longer chunk."""

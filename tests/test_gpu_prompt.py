@@ -159,6 +159,24 @@ def test_plan_advances_lengths_in_place():
     assert ws.status() == 0
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_plan_and_release_of_the_most_requests(in_place):
+    """8192 requests, the limit of a call: sixteen strips of the scan, the whole of its shared memory."""
+    B, page = 8192, 16
+    rng = np.random.default_rng(12)
+    ctx, new = rng.integers(0, 100, B), rng.integers(0, 4, B)
+    held, free, count, table = state(rng, B, page, ctx, B // 2)
+    ref = check_plan(ctx, new, held, free, count, table, page, 2 * B, in_place)
+    assert not ref["left"] and not ref["bad"] and ref["q_start"][-1] == new.sum() > B  # 1.5 tokens a request
+    done = (rng.random(B) < 0.5).astype(np.int32)
+    st = prompt.PageState(i32(ref["table"]), i32(free), i32([ref["count"]]), i32(ref["held"]), page, len(free))
+    ws = prompt.status_workspace(DEV)
+    prompt.page_release(i32(done), st, st, ws)
+    stack, top, kept = op.release(done, ref["held"], free, ref["count"], ref["table"])
+    assert ws.status() == 0 and int(st.free_count) == top
+    assert np.array_equal(st.free.cpu().numpy(), stack) and np.array_equal(st.held.cpu().numpy(), kept)
+
+
 def test_release_of_a_state_that_does_not_fit():
     st = prompt.PageState.allocate(3, 4, 16, 10, DEV)
     ws = prompt.status_workspace(DEV)
