@@ -22,15 +22,19 @@
 // weights go out in halves, so that the product with V begins before the last
 // of them. At that size the card is at its power limit (1.64 GHz): 1.09 to 1.15
 // of the 1.38 PFLOP/s that a library product sustains there. 64 single tokens
-// on 4k to 32k keys: 6.8 TB/s.
+// on 4k to 32k keys: 6.8 TB/s in short runs, 6.0 at the power limit. The size of
+// the pages does not matter much: 16 to 256 rows, the same within 1 %.
 //
 // Items of at most 128 rows (single tokens, short chunks) have one row tile;
 // its key tiles then go to the two softmax groups in turn, each with its own
 // O, joined at the item's end: two tiles in flight hide the softmax latency.
 //
 // The row maximum a weight refers to is only moved when a score passes it by
-// 2^8 (weights up to 2^8 are as exact as below 1, and fp32 sums hold them), so
-// O is rarely rescaled.
+// 2^8, a known refinement of the running softmax (weights up to 2^8 are as
+// exact as below 1, and fp32 sums hold them), so O is rarely rescaled.
+//
+// Every wait is bounded, a warp's lanes give up together, and what is under way
+// then lands before the CTA ends.
 #pragma once
 
 #include <cuda_bf16.h>

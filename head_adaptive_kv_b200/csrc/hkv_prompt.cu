@@ -793,7 +793,7 @@ hkv_status hkv_qk_norm_rope(const hkv_problem *prob, const void *q, int64_t q_st
     P.mscale = rope->mscale;
     P.status = static_cast<uint32_t *>(ws);
     const cudaStream_t st = (cudaStream_t)stream;
-    // One token a CTA while that leaves SMs free; else eight, whose K and V rows then lie side by side in a page
+    // One token a CTA while that leaves some of the 148 SMs free; else eight, whose K and V rows then lie side by side in a page
     // (16384 tokens of 32 + 2 x 8 bf16 heads of 128: 78 us, 81 with four, 84 with 32).
     const int tb = tokens < 4 * 148 ? 1 : 8;
     const int64_t grid = (tokens + tb - 1) / tb;

@@ -318,7 +318,8 @@ def page_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, state: PageState, af
 
 
 def page_release(done: torch.Tensor, state: PageState, after: PageState, ws: StatusWorkspace, stream=None):
-    """The pages of the requests with done[b] != 0 (int32 [B]) go back on the stack."""
+    """The pages of the requests with done[b] != 0 (int32 [B]) go back on the stack, each as often as it stands in their
+    tables: a page that several requests share must go back with one of them only. See hkv_page_release."""
     B = state._rows
     _int32(done, B, "done")
     state._same_pool(after)
@@ -356,7 +357,7 @@ def qk_norm_rope(prob: Problem, q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
     """Per-head RMS norm (with q_weight and k_weight, [D]; left out without them) and position rotation of the
     projected rows q [tokens, Hq, D], k and v [tokens, Hkv, D] at positions pos (int32 [tokens], -1 = skipped row).
     q goes to q_out; k and v to the slots of the pages (pages and slot) or to k_out and v_out, as hkv.append takes
-    them. See hkv_qk_norm_rope."""
+    them. Contiguous q, k and v may be their own outputs. See hkv_qk_norm_rope."""
     T, D, dtype = q.shape[0], prob.D, prob.dtype
     qs = _rows(q, dtype, (T, prob.Hq, D), "q")
     ks = _rows(k, dtype, (T, prob.Hkv, D), "k")
@@ -390,7 +391,8 @@ def chunk_attention(prob: Problem, q: torch.Tensor, q_start: torch.Tensor, kv_le
                     out: torch.Tensor, ws: ChunkWorkspace, lse: Optional[torch.Tensor] = None, stream=None):
     """Attention of a chunk of new tokens over the paged cache: rows q_start[b] .. q_start[b+1]-1 of q are the last
     tokens of request b, whose kv_len[b] tokens (those included) are in the pages; each attends up to its own
-    position. q, out: [tokens, Hq, D] (out contiguous); lse: optional fp32 [tokens, Hq]. See hkv_chunk_attention."""
+    position. q, out: [tokens, Hq, D] (out contiguous, apart from q); lse: optional fp32 [tokens, Hq]. See
+    hkv_chunk_attention."""
     T = q.shape[0]
     shape = (T, prob.Hq, prob.D)
     qs = _rows(q, prob.dtype, shape, "q")

@@ -105,7 +105,11 @@ hkv_status hkv_page_plan(int32_t B, const int32_t *ctx_len, const int32_t *new_l
  * but this call writes `free` above free_count. A state that does not fit the pool
  * (a held count below 0 or above the table's columns, more pages than the
  * stack has room for, a table entry to go back that is no page of the pool) sets
- * HKV_DEV_BAD_INDEX and releases nothing. */
+ * HKV_DEV_BAD_INDEX and releases nothing. The call knows no shared pages: one that
+ * stands in several tables (a common prefix) goes back with each of them, and
+ * would then be given to two requests. Of requests that share pages only one may
+ * be released, after the others are done with them; the pages that the others
+ * hold alone are the caller's to put on the stack. */
 hkv_status hkv_page_release(int32_t B, const int32_t *done, const hkv_pages *pages, const hkv_page_state *in,
                             const hkv_page_state *after, void *ws, size_t ws_bytes, hkv_stream_t stream);
 
@@ -170,7 +174,13 @@ hkv_status hkv_chunk_workspace_size(const hkv_problem *prob, int32_t tokens, siz
  * - Sums and softmax statistics are fp32. With bf16 the weights are rounded to
  *   bf16 for the product with V, and out once at its end.
  * - ws: hkv_chunk_workspace_size bytes for at least `tokens` rows, zeroed once
- *   by hkv_workspace_init, and again after HKV_DEV_TIMEOUT. Two kernels. */
+ *   by hkv_workspace_init, and again after HKV_DEV_TIMEOUT. Two kernels; a wait in
+ *   them ends after 2^31 ns at the latest, whatever hkv_set_wait_limit_ns allows.
+ * - fp32 has a kernel for single tokens and one for chunks, chosen by the host, which
+ *   does not see the lengths: the first when tokens <= B. Results are right either
+ *   way, but single tokens in a step with room for more rows take up to 3.6 times
+ *   as long, as does a long chunk in a step with no more rows than requests (2.4
+ *   times). bf16 has one kernel for both. */
 hkv_status hkv_chunk_attention(const hkv_problem *prob, const void *q, int64_t q_stride, int32_t tokens,
                                const int32_t *q_start, const int32_t *kv_len, const hkv_pages *pages, void *out,
                                float *lse, void *ws, size_t ws_bytes, hkv_stream_t stream);
