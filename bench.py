@@ -49,17 +49,24 @@ def peaks():
         return 6650.0, "fallback"
 
 
+def kernel_sources():
+    """The step's source and the kernel sources it includes: what the timed kernels are compiled from."""
+    from head_adaptive_kv_b200 import build
+
+    return sorted(f for f in build._inputs(os.path.join(build.CSRC, "hkv_api.cu")) if os.path.dirname(f) == build.CSRC)
+
+
 def csrc_hash() -> str:
-    """Hash of the kernel sources with comments and blank space removed, so a
-    profile stays attached to its kernels across comment-only edits."""
+    """Hash of the step's kernel sources with comments and blank space removed, so a
+    profile stays attached to its kernels across comment-only edits and changes of
+    other kernels."""
     h = hashlib.sha256()
-    d = os.path.join(ROOT, "head_adaptive_kv_b200", "csrc")
-    for f in sorted(os.listdir(d)):
-        with open(os.path.join(d, f), encoding="utf-8") as fh:
+    for f in kernel_sources():
+        with open(f, encoding="utf-8") as fh:
             text = fh.read()
         text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
         text = re.sub(r"//[^\n]*", " ", text)
-        h.update(f.encode() + " ".join(text.split()).encode())
+        h.update(os.path.basename(f).encode() + " ".join(text.split()).encode())
     return h.hexdigest()[:16]
 
 

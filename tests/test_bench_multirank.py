@@ -64,3 +64,13 @@ def test_step_bytes_counts_scored_and_attended_rows():
     # dense and condensed K and V; selected tokens: V row and logit record
     attended = U * (256 + 64) * 2 * 128 * 2 + U * 2048 * (128 * 2 + 16)
     assert b - scored - attended == wl.B * wl.Hq * 128 * 2 + wl.B * wl.Hq * 129 * 4 + U * 2048 * 4 + U * 4
+
+
+def test_traffic_record_belongs_to_the_timed_kernels():
+    """The profile's DRAM bytes hold for the sources that the step's kernels are compiled from: other kernels of the
+    library change none of them."""
+    import bench
+
+    names = [os.path.basename(f) for f in bench.kernel_sources()]
+    assert {"hkv_api.cu", "hkv_kernels.cuh", "hkv_device.cuh"} <= set(names)
+    assert not any("chunk" in n or "prompt" in n for n in names)
