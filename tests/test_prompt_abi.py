@@ -181,11 +181,11 @@ def test_chunk_attention_refuses_outputs_over_queries(pr, hk):
     prob = _prob(hk)  # rows of 8 heads of 128 in bf16: 2048 bytes of q and out, 32 of lse
     at = dict(q=A, out=2 * A, lse=3 * A, T=5, nbytes=0)  # (what passes gets as far as the workspace)
     for what, kw in {"in place": dict(out=A), "a row further": dict(out=A + 2048), "up to the last row": dict(out=A + 8192),
-                     "strided": dict(q=A, qs=1536, out=A + 4 * 3072 + 2032), "from before": dict(out=A - 5 * 2048 + 16),
+                     "strided": dict(q=A, qs=1280, out=A + 4 * 2560 + 2032), "from before": dict(out=A - 5 * 2048 + 16),
                      "lse on q": dict(lse=A + 16), "lse on out": dict(lse=2 * A + 5 * 2048 - 4)}.items():
         assert _attn(pr, prob, **{**at, **kw}) == 1, what
     for what, kw in {"apart": dict(), "no lse": dict(lse=None), "behind": dict(out=A + 5 * 2048), "before": dict(out=A - 5 * 2048),
-                     "strided": dict(qs=1536, out=A + 4 * 3072 + 2048), "lse behind": dict(lse=2 * A + 5 * 2048)}.items():
+                     "strided": dict(qs=1280, out=A + 4 * 2560 + 2048), "lse behind": dict(lse=2 * A + 5 * 2048)}.items():
         assert _attn(pr, prob, **{**at, **kw}) == 6, what
 
 
